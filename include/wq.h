@@ -92,7 +92,9 @@ typedef enum {
     WQ_ERR_TUNING = -8,    /* tuning file unreadable or malformed */
     WQ_ERR_TIMEOUT = -9,   /* a bounded device-side wait gave up */
     WQ_ERR_ARCH = -10,     /* device is not sm_100 (B200 class) */
-    WQ_ERR_VARIANT = -11   /* forced variant / split not valid for the shape */
+    WQ_ERR_VARIANT = -11,  /* forced variant / split not valid for the shape */
+    WQ_ERR_EPILOGUE = -12, /* unknown activation, or an epilogue row stride below N */
+    WQ_ERR_DTYPE = -13     /* unknown element type of the logits */
 } wq_status;
 
 /* Kernel variants (wq_linear_forced, wq_get_choice). */
@@ -112,6 +114,18 @@ typedef enum {
 #define WQ_VARIANT_GEMM_W4 6 /* W4A16 only, M <= 128: stream-K tcgen05 GEMM with one CTA per SM
                                 (16 warps; 20 at 64 tokens), every role (weight and x loads, dequantization, MMA, group
                                 rescale) on its own warps with its own ring; needs the workspace */
+
+/* Activations of the layer's epilogue (wq_epilogue). */
+#define WQ_ACT_NONE 0
+#define WQ_ACT_RELU 1
+#define WQ_ACT_GELU 2      /* v (1 + erf(v / sqrt 2)) / 2 */
+#define WQ_ACT_GELU_TANH 3 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+#define WQ_ACT_SILU 4      /* v / (1 + exp(-v)) */
+
+/* Element types of the logits of wq_logprobs. */
+#define WQ_DTYPE_BF16 0
+#define WQ_DTYPE_F16 1
+#define WQ_DTYPE_F32 2
 
 /* Static description of a status code. Host. Never NULL. */
 const char *wq_strerror(int status);
@@ -214,6 +228,45 @@ int wq_linear(const uint16_t *x, int M, int K, const void *Wq, const void *scale
 int wq_linear_f16(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
                   const void *zeros, int group, int N, uint16_t *y, cudaStream_t stream);
 
+/* What follows a layer's product, in the order it is applied; NULL leaves a
+ * part out.  The operands have the activations' type.
+ *   bias      device, [N], one value per output channel
+ *   act       WQ_ACT_*
+ *   mul       device, M rows of N values, ld_mul elements apart (>= N): the
+ *             other half of a gated feed-forward layer
+ *   residual  device, M rows of N values, ld_residual elements apart (>= N)
+ * The row strides are not looked at for a NULL operand, or for M = 1. */
+typedef struct {
+    const uint16_t *bias;
+    const uint16_t *mul;
+    const uint16_t *residual;
+    int64_t ld_mul;
+    int64_t ld_residual;
+    int act;
+} wq_epilogue;
+
+/* The layer with its epilogue in the same kernel:
+ *     y = act(x . dequant(Wq)^T + bias) * mul + residual
+ * x, y bf16; the epilogue in fp32 on the fp32-accumulated sum (the integer
+ * paths' binary64 sum), rounded once.  The operands need element alignment
+ * only.  y may be the residual or mul buffer itself (same address, row stride
+ * N: the residual stream updated in place); it must not overlap them, or x,
+ * in any other way.
+ *   epilogue  host, required; with every part absent the call is wq_linear
+ *   ws        a workspace of ws_bytes for this call, as wq_linear_ex (zeroed by
+ *             the caller before its first use; calls that share one must not
+ *             overlap), or NULL: the registered one
+ * Kernels, chunks and the workspace are the dispatcher's, as in wq_linear;
+ * WQ_ERR_EPILOGUE for an unknown act or a row stride below N. */
+int wq_linear_epilogue(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
+                       const void *zeros, int group, int N, const wq_epilogue *epilogue,
+                       uint16_t *y, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* wq_linear_f16 with an epilogue, its operands and y fp16.  No workspace. */
+int wq_linear_epilogue_f16(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
+                           const void *zeros, int group, int N, const wq_epilogue *epilogue,
+                           uint16_t *y, cudaStream_t stream);
+
 /* wq_linear with an explicit kernel variant (WQ_VARIANT_*) and split factor.
  * variant = WQ_VARIANT_AUTO, or split = 0, leaves that choice to the dispatcher.
  * GEMV: split = CTAs per SM, 1..4, capped by occupancy (the K range of
@@ -273,6 +326,48 @@ int wq_linear_topk(const uint16_t *x, int M, int K, const void *Wq, const void *
 
 /* Scratch bytes of wq_linear_topk; 0 for arguments out of its limits. Host. */
 size_t wq_topk_workspace_bytes(int M, int N, int k);
+
+/* Log probabilities of given tokens, the entropy and the k most likely
+ * alternatives of M rows of N logits, in one pass over them:
+ *     lse = log sum_n exp(x[n])   (fp32, about the row's maximum)
+ *   logits    device, M rows of N values of type dtype (WQ_DTYPE_*), ld
+ *             elements apart (ld >= N; not looked at for M = 1), any element
+ *             alignment
+ *   tokens    device, int32 [M], or NULL together with logprob
+ *   k         alternatives per row, 0 (none) .. 64, at most N
+ *   logprob   device, fp32 [M]: x[tokens[m]] - lse; NaN for a token outside
+ *             [0, N), which names no logit
+ *   entropy   device, fp32 [M] or NULL: -sum_n p log p, in nats
+ *   top_logprobs, top_idx   device, fp32 and int32 [M][k] (k = 0: not looked
+ *             at): the k largest logits, descending, as x - lse, and their
+ *             indices; the lower index first among equal logits (-0 = +0)
+ * A logit of -inf has probability 0, log probability -inf and no part in the
+ * entropy.  A row of nothing but -inf, or with a NaN or +inf, has no
+ * distribution: its log probabilities and entropy are NaN, its indices are
+ * still those of the largest logits (a NaN above +inf).
+ * 1 <= M <= 65536, 1 <= N <= 1048576.  Needs no workspace.  The
+ * sums are taken in an order fixed by M, N, k and the device: equal calls give
+ * equal bits.  WQ_ERR_NULL if nothing is asked for. */
+int wq_logprobs(const void *logits, int dtype, int M, int N, int64_t ld, const int32_t *tokens,
+                int k, float *logprob, float *entropy, float *top_logprobs, int32_t *top_idx,
+                cudaStream_t stream);
+
+/* wq_logprobs of the logits x . dequant(Wq)^T of a quantized vocabulary head,
+ * which are formed in fp32 and never rounded to 16 bits or returned.
+ *   scratch   device, at least wq_linear_logprobs_workspace_bytes(M, N) bytes,
+ *             16-byte aligned, owned by the caller: the fp32 logits of up to
+ *             512 tokens at a time, in turn
+ *   ws        as wq_linear_epilogue
+ * Other arguments as wq_linear and wq_logprobs; WQ_ERR_WORKSPACE for a scratch
+ * that is too small. */
+int wq_linear_logprobs(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
+                       const void *zeros, int group, int N, const int32_t *tokens, int k,
+                       float *logprob, float *entropy, float *top_logprobs, int32_t *top_idx,
+                       void *scratch, size_t scratch_bytes, void *ws, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/* Scratch bytes of wq_linear_logprobs; 0 for arguments out of its limits. Host. */
+size_t wq_linear_logprobs_workspace_bytes(int M, int N);
 
 /* Bytes of workspace for M tokens, a K x N weight and GEMM splits up to
  * max_split: enough for every variant of that shape (M > 128: of its

@@ -35,8 +35,20 @@ WQ_VARIANT_GEMM_W4 = 6  # W4A16 stream-K tcgen05 GEMM, one role-split CTA per SM
 STATUS = {
     0: "WQ_OK", -1: "WQ_ERR_NULL", -2: "WQ_ERR_SHAPE", -3: "WQ_ERR_ALIGN", -4: "WQ_ERR_GROUP",
     -5: "WQ_ERR_HEADER", -6: "WQ_ERR_WORKSPACE", -7: "WQ_ERR_CUDA", -8: "WQ_ERR_TUNING",
-    -9: "WQ_ERR_TIMEOUT", -10: "WQ_ERR_ARCH", -11: "WQ_ERR_VARIANT",
+    -9: "WQ_ERR_TIMEOUT", -10: "WQ_ERR_ARCH", -11: "WQ_ERR_VARIANT", -12: "WQ_ERR_EPILOGUE", -13: "WQ_ERR_DTYPE",
 }
+
+# activations of the layer's epilogue
+WQ_ACT_NONE = 0
+WQ_ACT_RELU = 1
+WQ_ACT_GELU = 2
+WQ_ACT_GELU_TANH = 3
+WQ_ACT_SILU = 4
+
+# element types of wq_logprobs
+WQ_DTYPE_BF16 = 0
+WQ_DTYPE_F16 = 1
+WQ_DTYPE_F32 = 2
 
 
 class WQError(RuntimeError):
@@ -67,6 +79,11 @@ def _load():
         "wq_linear_noalloc": (I, [P, I, I, P, P, P, I, I, P, P]),
         "wq_linear_topk": (I, [P, I, I, P, P, P, I, I, I, P, P, P, SZ, P]),
         "wq_linear_f16": (I, [P, I, I, P, P, P, I, I, P, P]),
+        "wq_linear_epilogue": (I, [P, I, I, P, P, P, I, I, P, P, P, SZ, P]),
+        "wq_linear_epilogue_f16": (I, [P, I, I, P, P, P, I, I, P, P, P]),
+        "wq_logprobs": (I, [P, I, I, I, ctypes.c_int64, P, I, P, P, P, P, P]),
+        "wq_linear_logprobs": (I, [P, I, I, P, P, P, I, I, P, I, P, P, P, P, P, SZ, P, SZ, P]),
+        "wq_linear_logprobs_workspace_bytes": (SZ, [I, I]),
         "wq_topk_workspace_bytes": (SZ, [I, I, I]),
         "wq_workspace_bytes": (SZ, [I, I, I, I]),
         "wq_set_workspace": (I, [P, SZ]),
@@ -268,6 +285,179 @@ def wq_linear_f16(x: torch.Tensor, pw: PackedWeight, y: Optional[torch.Tensor] =
     _check(lib.wq_linear_f16(_p(x), M, K, _p(pw.wq), _p(pw.scales), _p(pw.zeros), pw.group, pw.N, _p(y),
                              _s(stream)), "wq_linear_f16")
     return y
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ld_mul", ctypes.c_int64), ("ld_residual", ctypes.c_int64), ("act", ctypes.c_int)]
+
+
+def _refuse(status: int, what: str) -> None:
+    raise WQError(status, what)
+
+
+def _rows(t: torch.Tensor, shape, dtype, device, what: str) -> int:
+    """Row stride in elements of a 2-D operand whose rows are contiguous."""
+    if t.dtype != dtype:
+        _refuse(-13, f"{what} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
+        _refuse(-2, f"{what} {tuple(t.shape)} strides {tuple(t.stride())}, not rows of {tuple(shape)}")
+    if t.device != device:
+        _refuse(-2, f"{what} is on {t.device}, not {device}")
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, n: int, dtype, device, what: str) -> None:
+    if t.dtype != dtype:
+        _refuse(-13, f"{what} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        _refuse(-2, f"{what} {tuple(t.shape)} strides {tuple(t.stride())}, not contiguous ({n},)")
+    if t.device != device:
+        _refuse(-2, f"{what} is on {t.device}, not {device}")
+
+
+class _on:
+    """Makes x's device and the stream the call runs on (a torch stream or a
+    raw handle; None: the device's current one) current for the block, so that
+    outputs are allocated for the stream that writes them.  Yields the
+    stream's handle."""
+
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
+            _refuse(-2, f"tensors on {device}, not on a CUDA device")
+        self._contexts = ()
+        if stream is not None or torch.cuda.current_device() != device.index:
+            if stream is not None and not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self._contexts = (torch.cuda.device(device), torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self._contexts:
+            c.__enter__()
+        return _s(None)
+
+    def __exit__(self, *exc):
+        for c in reversed(self._contexts):
+            c.__exit__(*exc)
+
+
+def _layer_input(x: torch.Tensor, pw: PackedWeight, dtype, what: str) -> None:
+    if x.dtype != dtype:
+        _refuse(-13, f"{what}: x is {x.dtype}, not {dtype}")
+    if x.dim() != 2 or x.shape[1] != pw.K or not x.is_contiguous():
+        _refuse(-2, f"{what}: x {tuple(x.shape)} strides {tuple(x.stride())}, not contiguous [M][{pw.K}]")
+    if pw.wq.device != x.device:
+        _refuse(-2, f"{what}: x on {x.device}, the weight on {pw.wq.device}")
+
+
+def _scratch(ws: Optional[torch.Tensor], device, what: str):
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        _refuse(-2, f"{what}: a contiguous buffer on {device} is wanted")
+    return _p(ws), ws.numel() * ws.element_size()
+
+
+def _epilogue(x, pw, bias, act, mul, residual, y, what):
+    M, dtype, dev = x.shape[0], x.dtype, x.device
+    e = _Epilogue(act=int(act))
+    if bias is not None:
+        _vector(bias, pw.N, dtype, dev, f"{what}: bias")
+        e.bias = bias.data_ptr()
+    if mul is not None:
+        e.ld_mul = _rows(mul, (M, pw.N), dtype, dev, f"{what}: mul")
+        e.mul = mul.data_ptr()
+    if residual is not None:
+        e.ld_residual = _rows(residual, (M, pw.N), dtype, dev, f"{what}: residual")
+        e.residual = residual.data_ptr()
+    if y is None:
+        y = torch.empty((M, pw.N), dtype=dtype, device=dev)
+    elif _rows(y, (M, pw.N), dtype, dev, f"{what}: y") != pw.N and M > 1:
+        _refuse(-2, f"{what}: y is not contiguous")
+    return e, y
+
+
+def wq_linear_epilogue(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor] = None,
+                       act: int = WQ_ACT_NONE, mul: Optional[torch.Tensor] = None,
+                       residual: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                       y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = act(x . dequant(W)^T + bias) * mul + residual, one rounding; x bf16
+    [M][K], bias [N], mul and residual [M][N] (rows may be strided), all bf16.
+    y may be residual or mul themselves.  ws: this call's workspace (zeroed
+    before its first use), else the registered one."""
+    _layer_input(x, pw, torch.bfloat16, "wq_linear_epilogue")
+    with _on(x.device, stream) as s:
+        e, y = _epilogue(x, pw, bias, act, mul, residual, y, "wq_linear_epilogue")
+        w, nbytes = _scratch(ws, x.device, "wq_linear_epilogue: ws")
+        _check(lib.wq_linear_epilogue(_p(x), x.shape[0], pw.K, _p(pw.wq), _p(pw.scales), _p(pw.zeros), pw.group, pw.N,
+                                      ctypes.byref(e), _p(y), w, nbytes, s), "wq_linear_epilogue")
+    return y
+
+
+def wq_linear_epilogue_f16(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor] = None,
+                           act: int = WQ_ACT_NONE, mul: Optional[torch.Tensor] = None,
+                           residual: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                           y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """wq_linear_epilogue with fp16 activations, operands and outputs (ws is
+    not needed and not looked at)."""
+    _layer_input(x, pw, torch.float16, "wq_linear_epilogue_f16")
+    with _on(x.device, stream) as s:
+        e, y = _epilogue(x, pw, bias, act, mul, residual, y, "wq_linear_epilogue_f16")
+        _check(lib.wq_linear_epilogue_f16(_p(x), x.shape[0], pw.K, _p(pw.wq), _p(pw.scales), _p(pw.zeros), pw.group,
+                                          pw.N, ctypes.byref(e), _p(y), s), "wq_linear_epilogue_f16")
+    return y
+
+
+_LOGIT_DTYPES = {torch.bfloat16: WQ_DTYPE_BF16, torch.float16: WQ_DTYPE_F16, torch.float32: WQ_DTYPE_F32}
+
+
+def _logprob_outputs(M: int, tokens, k: int, device, what: str):
+    if tokens is not None:
+        _vector(tokens, M, torch.int32, device, f"{what}: tokens")
+    if k < 0:
+        _refuse(-2, f"{what}: k = {k}")
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
+    return (None if tokens is None else new((M,), torch.float32), new((M,), torch.float32),
+            new((M, k), torch.float32) if k else None, new((M, k), torch.int32) if k else None)
+
+
+def wq_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, k: int = 0, stream=None):
+    """(logprob [M] of the tokens, entropy [M], top_logprobs [M][k], top_idx
+    [M][k] int32) of rows of logits (bf16, fp16 or fp32 [M][N], rows may be
+    strided); fp32 but for the indices.  tokens int32 [M]; without them the
+    first is None, with k = 0 the last two are."""
+    if logits.dtype not in _LOGIT_DTYPES:
+        _refuse(-13, f"wq_logprobs: logits are {logits.dtype}")
+    if logits.dim() != 2:
+        _refuse(-2, f"wq_logprobs: logits {tuple(logits.shape)}, not [M][N]")
+    M, N = logits.shape
+    ld = _rows(logits, (M, N), logits.dtype, logits.device, "wq_logprobs: logits")
+    with _on(logits.device, stream) as s:
+        logprob, entropy, top, idx = _logprob_outputs(M, tokens, k, logits.device, "wq_logprobs")
+        _check(lib.wq_logprobs(_p(logits), _LOGIT_DTYPES[logits.dtype], M, N, ld, _p(tokens), k, _p(logprob),
+                               _p(entropy), _p(top), _p(idx), s), "wq_logprobs")
+    return logprob, entropy, top, idx
+
+
+def wq_linear_logprobs_workspace_bytes(M: int, N: int) -> int:
+    return int(lib.wq_linear_logprobs_workspace_bytes(M, N))
+
+
+def wq_linear_logprobs(x: torch.Tensor, pw: PackedWeight, tokens: Optional[torch.Tensor], k: int,
+                       scratch: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None):
+    """wq_logprobs of the fp32 logits x . dequant(W)^T of a quantized
+    vocabulary head; scratch a device buffer of at least
+    wq_linear_logprobs_workspace_bytes(M, N) bytes, ws as wq_linear_epilogue."""
+    _layer_input(x, pw, torch.bfloat16, "wq_linear_logprobs")
+    M = x.shape[0]
+    with _on(x.device, stream) as s:
+        logprob, entropy, top, idx = _logprob_outputs(M, tokens, k, x.device, "wq_linear_logprobs")
+        sp, sbytes = _scratch(scratch, x.device, "wq_linear_logprobs: scratch")
+        w, nbytes = _scratch(ws, x.device, "wq_linear_logprobs: ws")
+        _check(lib.wq_linear_logprobs(_p(x), M, pw.K, _p(pw.wq), _p(pw.scales), _p(pw.zeros), pw.group, pw.N,
+                                      _p(tokens), k, _p(logprob), _p(entropy), _p(top), _p(idx), sp, sbytes, w, nbytes,
+                                      s), "wq_linear_logprobs")
+    return logprob, entropy, top, idx
 
 
 def wq_topk_workspace_bytes(M: int, N: int, k: int) -> int:

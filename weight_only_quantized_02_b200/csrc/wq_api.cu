@@ -201,9 +201,10 @@ int lookup_choice(const DeviceInfo &d, int M, int K, int N, int bits, int group,
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA; }
 
 // One call of at most kChunkTokens tokens: the dispatcher's (or the forced)
-// kernel for this M.
+// kernel for this M, with its epilogue (NULL: none).
 int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros, int group,
-                 int N, uint16_t *y, int variant, int split, void *ws, size_t ws_bytes_given, cudaStream_t stream)
+                 int N, uint16_t *y, int variant, int split, void *ws, size_t ws_bytes_given, cudaStream_t stream,
+                 const EpiArgs *epi = nullptr)
 {
     int bits = 0;
     int st = bits_of_group(group, &bits);
@@ -277,7 +278,7 @@ int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *sc
     if (!choice_valid(c.variant, c.split, M, K, bits, lg))
         return WQ_ERR_VARIANT;
 
-    LinearArgs a{x, M, K, N, Wq, scales, zeros, bits, bits == 8 ? 0 : lg, y};
+    LinearArgs a{x, M, K, N, Wq, scales, zeros, bits, bits == 8 ? 0 : lg, y, epi};
     if (c.variant == WQ_VARIANT_GEMV_I8) {
         if (!gi_ws_ok)
             return WQ_ERR_WORKSPACE;
@@ -311,6 +312,17 @@ int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *sc
     return cuda_status(launch_gemm(a, c.split, c.split > 1 ? w : nullptr, d.sm_count, stream));
 }
 
+// The epilogue of the token rows from m0 on.
+EpiArgs epi_rows_from(const EpiArgs &e, int m0)
+{
+    EpiArgs r = e;
+    if (r.mul)
+        r.mul += (long long)m0 * r.ld_mul;
+    if (r.res)
+        r.res += (long long)m0 * r.ld_res;
+    return r;
+}
+
 // The layer for any M up to kMaxTokens: runs of kChunkTokens tokens, one
 // kernel each, in order on the stream (x and y advance by whole token rows,
 // so every chunk keeps their 16-byte alignment).  Each chunk streams the
@@ -318,25 +330,45 @@ int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *sc
 // failing chunk returns its status; the chunks before it are already
 // enqueued.
 int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros, int group,
-                int N, uint16_t *y, int variant, int split, void *ws, size_t ws_bytes_given, cudaStream_t stream)
+                int N, uint16_t *y, int variant, int split, void *ws, size_t ws_bytes_given, cudaStream_t stream,
+                const EpiArgs *epi = nullptr)
 {
     int bits = 0;
     if (bits_of_group(group, &bits) != WQ_OK)
         return WQ_ERR_GROUP;
     const int chunk = chunk_tokens(bits, lgroup_of(bits, K, group));
     if (M <= chunk)
-        return linear_chunk(x, M, K, Wq, scales, zeros, group, N, y, variant, split, ws, ws_bytes_given, stream);
+        return linear_chunk(x, M, K, Wq, scales, zeros, group, N, y, variant, split, ws, ws_bytes_given, stream, epi);
     if (M > kMaxTokens)
         return WQ_ERR_SHAPE;
     if (!x || !y)
         return WQ_ERR_NULL;
     for (int m0 = 0; m0 < M; m0 += chunk) {
         const int mc = std::min(chunk, M - m0);
-        const int st = linear_chunk(x + (size_t)m0 * K, mc, K, Wq, scales, zeros, group, N, y + (size_t)m0 * N,
-                                    variant, split, ws, ws_bytes_given, stream);
+        EpiArgs ec;
+        if (epi)
+            ec = epi_rows_from(*epi, m0);
+        const size_t y_off = (size_t)m0 * N * (epi && epi->out_f32 ? 2 : 1); // in 16-bit units
+        const int st = linear_chunk(x + (size_t)m0 * K, mc, K, Wq, scales, zeros, group, N, y + y_off, variant, split,
+                                    ws, ws_bytes_given, stream, epi ? &ec : nullptr);
         if (st != WQ_OK)
             return st;
     }
+    return WQ_OK;
+}
+
+// The caller's epilogue as the kernels take it; false status for one whose
+// rows are narrower than the output's or whose activation is unknown.
+int epi_args(const wq_epilogue *e, int M, int N, EpiArgs *out)
+{
+    if (e->act < WQ_ACT_NONE || e->act > WQ_ACT_SILU)
+        return WQ_ERR_EPILOGUE;
+    if ((e->mul && M > 1 && e->ld_mul < N) || (e->residual && M > 1 && e->ld_residual < N))
+        return WQ_ERR_EPILOGUE;
+    if ((reinterpret_cast<uintptr_t>(e->bias) | reinterpret_cast<uintptr_t>(e->mul) |
+         reinterpret_cast<uintptr_t>(e->residual)) & 1u)
+        return WQ_ERR_ALIGN;
+    *out = EpiArgs{e->bias, e->mul, e->residual, (long long)e->ld_mul, (long long)e->ld_residual, e->act, 0};
     return WQ_OK;
 }
 
@@ -408,6 +440,8 @@ const char *wq_strerror(int status)
     case WQ_ERR_TUNING: return "tuning file unreadable or malformed";
     case WQ_ERR_TIMEOUT: return "a bounded device-side wait gave up";
     case WQ_ERR_ARCH: return "device is not sm_100 (B200 class)";
+    case WQ_ERR_EPILOGUE: return "unknown activation, or epilogue rows closer together than N";
+    case WQ_ERR_DTYPE: return "unknown element type of the logits";
     case WQ_ERR_VARIANT: return "forced variant/split not valid for this shape";
     default: return "unknown status";
     }
@@ -542,8 +576,23 @@ int wq_linear_noalloc(const uint16_t *x, int M, int K, const void *Wq, const voi
     return cuda_status(launch_gemv_sk_noalloc(a, d.sm_count, stream));
 }
 
-int wq_linear_f16(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros, int group,
-                  int N, uint16_t *y, cudaStream_t stream)
+int wq_linear_epilogue(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros,
+                       int group, int N, const wq_epilogue *epilogue, uint16_t *y, void *ws, size_t ws_bytes_given,
+                       cudaStream_t stream)
+{
+    if (!epilogue)
+        return WQ_ERR_NULL;
+    EpiArgs e;
+    const int st = epi_args(epilogue, M, N, &e);
+    if (st != WQ_OK)
+        return st;
+    return linear_impl(x, M, K, Wq, scales, zeros, group, N, y, WQ_VARIANT_AUTO, 0, ws, ws_bytes_given, stream, &e);
+}
+
+} // extern "C"
+
+static int linear_f16_impl(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros,
+                           int group, int N, uint16_t *y, cudaStream_t stream, const EpiArgs *epi)
 {
     int bits = 0;
     int st = bits_of_group(group, &bits);
@@ -565,11 +614,35 @@ int wq_linear_f16(const uint16_t *x, int M, int K, const void *Wq, const void *s
     const int lg = lgroup_of(bits, K, group), ks = default_rb_slices(K, N, d.sm_count);
     for (int m0 = 0; m0 < M; m0 += 32) { // the row-block GEMV: 32 tokens per launch
         const int mc = std::min(32, M - m0);
-        LinearArgs a{x + (size_t)m0 * K, mc, K, N, Wq, scales, zeros, bits, bits == 8 ? 0 : lg, y + (size_t)m0 * N};
+        EpiArgs ec;
+        if (epi)
+            ec = epi_rows_from(*epi, m0);
+        LinearArgs a{x + (size_t)m0 * K, mc, K, N, Wq, scales, zeros, bits, bits == 8 ? 0 : lg, y + (size_t)m0 * N,
+                     epi ? &ec : nullptr};
         if ((st = cuda_status(launch_gemv(a, ks, d.sm_count, stream, true))) != WQ_OK)
             return st;
     }
     return WQ_OK;
+}
+
+extern "C" {
+
+int wq_linear_f16(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros, int group,
+                  int N, uint16_t *y, cudaStream_t stream)
+{
+    return linear_f16_impl(x, M, K, Wq, scales, zeros, group, N, y, stream, nullptr);
+}
+
+int wq_linear_epilogue_f16(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros,
+                           int group, int N, const wq_epilogue *epilogue, uint16_t *y, cudaStream_t stream)
+{
+    if (!epilogue)
+        return WQ_ERR_NULL;
+    EpiArgs e;
+    const int st = epi_args(epilogue, M, N, &e);
+    if (st != WQ_OK)
+        return st;
+    return linear_f16_impl(x, M, K, Wq, scales, zeros, group, N, y, stream, &e);
 }
 
 size_t wq_topk_workspace_bytes(int M, int N, int k)
@@ -600,6 +673,89 @@ int wq_linear_topk(const uint16_t *x, int M, int K, const void *Wq, const void *
         return st;
     void *cand = static_cast<uint8_t *>(ws) + ((size_t)M * N * 2 + 255) / 256 * 256;
     return cuda_status(launch_topk(logits, M, N, k, cand, vals, idx, stream));
+}
+
+static int check_logprobs(int M, int N, int k, const int32_t *tokens, const float *logprob, const float *entropy,
+                          const float *top, const int32_t *top_idx)
+{
+    if (M < 1 || M > kMaxTokens || N < 1 || N > kMaxN || k < 0 || k > kTopkMaxK || k > N)
+        return WQ_ERR_SHAPE;
+    if ((tokens == nullptr) != (logprob == nullptr) || (k > 0 && (!top || !top_idx)))
+        return WQ_ERR_NULL;
+    if (!logprob && !entropy && k == 0)
+        return WQ_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(logprob) |
+         reinterpret_cast<uintptr_t>(entropy) | reinterpret_cast<uintptr_t>(top) |
+         reinterpret_cast<uintptr_t>(top_idx)) & 3u)
+        return WQ_ERR_ALIGN;
+    return WQ_OK;
+}
+
+int wq_logprobs(const void *logits, int dtype, int M, int N, int64_t ld, const int32_t *tokens, int k, float *logprob,
+                float *entropy, float *top_logprobs, int32_t *top_idx, cudaStream_t stream)
+{
+    if (!logits)
+        return WQ_ERR_NULL;
+    if (dtype != WQ_DTYPE_BF16 && dtype != WQ_DTYPE_F16 && dtype != WQ_DTYPE_F32)
+        return WQ_ERR_DTYPE;
+    int st = check_logprobs(M, N, k, tokens, logprob, entropy, top_logprobs, top_idx);
+    if (st != WQ_OK)
+        return st;
+    if (M > 1 && ld < N)
+        return WQ_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(logits) & (dtype == WQ_DTYPE_F32 ? 3u : 1u))
+        return WQ_ERR_ALIGN;
+    DeviceInfo d;
+    if ((st = current_device_info(&d)) != WQ_OK)
+        return st;
+    if (d.major != 10)
+        return WQ_ERR_ARCH;
+    return cuda_status(launch_logprobs(logits, dtype, M, N, M > 1 ? ld : N, tokens, k, logprob, entropy, top_logprobs,
+                                       top_idx, d.sm_count, stream));
+}
+
+size_t wq_linear_logprobs_workspace_bytes(int M, int N)
+{
+    if (M < 1 || M > kMaxTokens || N < 1 || N > kMaxN)
+        return 0;
+    return (size_t)std::min(M, kHeadChunk) * N * sizeof(float);
+}
+
+int wq_linear_logprobs(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros,
+                       int group, int N, const int32_t *tokens, int k, float *logprob, float *entropy,
+                       float *top_logprobs, int32_t *top_idx, void *scratch, size_t scratch_bytes, void *ws,
+                       size_t ws_bytes_given, cudaStream_t stream)
+{
+    if (!x || !scratch)
+        return WQ_ERR_NULL;
+    int st = check_logprobs(M, N, k, tokens, logprob, entropy, top_logprobs, top_idx);
+    if (st != WQ_OK)
+        return st;
+    if (!aligned16(scratch))
+        return WQ_ERR_ALIGN;
+    const long long fit = (long long)(scratch_bytes / ((size_t)N * sizeof(float)));
+    if (fit < std::min(M, kHeadChunk))
+        return WQ_ERR_WORKSPACE;
+    DeviceInfo d;
+    if ((st = current_device_info(&d)) != WQ_OK)
+        return st;
+    EpiArgs e{};
+    e.out_f32 = 1;
+    float *logits = static_cast<float *>(scratch);
+    for (int m0 = 0; m0 < M; m0 += kHeadChunk) {
+        const int mc = std::min(kHeadChunk, M - m0);
+        st = linear_impl(x + (size_t)m0 * K, mc, K, Wq, scales, zeros, group, N, reinterpret_cast<uint16_t *>(logits),
+                         WQ_VARIANT_AUTO, 0, ws, ws_bytes_given, stream, &e);
+        if (st != WQ_OK)
+            return st;
+        st = cuda_status(launch_logprobs(logits, WQ_DTYPE_F32, mc, N, N, tokens ? tokens + m0 : nullptr, k,
+                                         logprob ? logprob + m0 : nullptr, entropy ? entropy + m0 : nullptr,
+                                         top_logprobs ? top_logprobs + (size_t)m0 * k : nullptr,
+                                         top_idx ? top_idx + (size_t)m0 * k : nullptr, d.sm_count, stream));
+        if (st != WQ_OK)
+            return st;
+    }
+    return WQ_OK;
 }
 
 size_t wq_workspace_bytes(int M, int K, int N, int max_split)

@@ -1,0 +1,156 @@
+// wq_epilogue.cuh -- the layer's epilogue, shared by every kernel that
+// writes y:
+//
+//     y[m][n] = round(act(v + bias[n]) * mul[m][n] + residual[m][n]),
+//
+// v the accumulated (and, for INT8, scaled) sum of output (m, n), everything
+// in fp32 and rounded once; or the fp32 value v itself (EpiArgs::out_f32, the
+// vocabulary head's unrounded logits).
+//
+// Kernels are instantiated without an epilogue (EPI = false: wq_linear's
+// code, unchanged) and with one, whose parts are chosen at run time by
+// branches that are the same for every thread.  A part costs one 16-bit load
+// per output (2 of the layer's bytes for every K bytes or K / 2 bytes of
+// weights), so what bounds the layer still does; the loads' latency, at the
+// end of a call, is what can be seen, and epi_load is therefore separate from
+// epi_store: a thread with several outputs loads all their operands first.
+//
+// y may be the residual or mul buffer itself (the same element): every
+// element is read and written by the same thread, and the operands are read
+// past L1 (ld.cg), so a line cached before another SM's write is never used.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "wq.h"
+#include "wq_internal.h"
+
+namespace wq {
+
+// The two tensor operands of one output, unrounded.
+struct EpiOps {
+    float mul, res;
+};
+
+template <bool F16>
+__device__ __forceinline__ float act16_to_float(uint16_t b)
+{
+    if constexpr (F16)
+        return __half2float(__ushort_as_half(b));
+    else
+        return __uint_as_float((uint32_t)b << 16);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint16_t float_to_act16(float v)
+{
+    if constexpr (F16)
+        return __half_as_ushort(__float2half_rn(v));
+    else
+        return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Out of line: five formulas inlined at every output of the unrolled stores
+// would multiply the kernels' code.  The erf form is written with erfc, which
+// keeps its relative accuracy where 1 + erf cancels; the tanh form is
+// v * logistic(2 u), which does not cancel either.
+static __device__ __noinline__ float epi_activation(float v, int act)
+{
+    if (act == WQ_ACT_RELU)
+        return v < 0.f ? 0.f : v;
+    if (act == WQ_ACT_GELU)
+        return 0.5f * v * erfcf(-0.70710678f * v);
+    float u = v; // WQ_ACT_SILU: v * logistic(v)
+    if (act == WQ_ACT_GELU_TANH)
+        u = 1.5957691f * fmaf(0.044715f * v, v * v, v); // 2 sqrt(2/pi) (v + 0.044715 v^3)
+    return v / (1.f + expf(-u));
+}
+
+// The operands of output (m, n); absent ones are the identity.
+template <bool EPI, bool F16 = false>
+__device__ __forceinline__ EpiOps epi_load(const EpiArgs &e, int m, int n)
+{
+    EpiOps o{1.f, 0.f};
+    if constexpr (EPI) {
+        if (e.mul)
+            o.mul = act16_to_float<F16>(__ldcg(e.mul + (long long)m * e.ld_mul + n));
+        if (e.res)
+            o.res = act16_to_float<F16>(__ldcg(e.res + (long long)m * e.ld_res + n));
+    }
+    return o;
+}
+
+template <bool EPI, bool F16 = false>
+__device__ __forceinline__ float epi_bias(const EpiArgs &e, int n)
+{
+    if constexpr (EPI)
+        if (e.bias)
+            return act16_to_float<F16>(__ldcg(e.bias + n));
+    return 0.f;
+}
+
+// act(v + bias) * mul + residual.  The sum v + bias and the product's fused
+// add round in fp32, 2^-24 relative each, far below the output's rounding.
+__device__ __forceinline__ float epi_value(const EpiArgs &e, float v, float bias, const EpiOps &o)
+{
+    v += bias;
+    if (e.act != WQ_ACT_NONE)
+        v = epi_activation(v, e.act);
+    return fmaf(v, o.mul, o.res);
+}
+
+// Writes output (m, n) with accumulated value v.
+template <bool EPI, bool F16 = false>
+__device__ __forceinline__ void epi_store(const EpiArgs &e, uint16_t *y, int N, int m, int n, float v, float bias,
+                                          const EpiOps &o)
+{
+    const size_t at = (size_t)m * N + n;
+    if constexpr (EPI) {
+        if (e.out_f32) {
+            reinterpret_cast<float *>(y)[at] = v;
+            return;
+        }
+        v = epi_value(e, v, bias, o);
+    }
+    y[at] = float_to_act16<F16>(v);
+}
+
+// The integer paths' form: v in binary64, rounded once where there is no
+// epilogue, to fp32 first where there is one.
+template <bool EPI>
+__device__ __forceinline__ void epi_store64(const EpiArgs &e, uint16_t *y, int N, int m, int n, double v, float bias,
+                                            const EpiOps &o)
+{
+    if constexpr (EPI)
+        epi_store<true>(e, y, N, m, n, (float)v, bias, o);
+    else
+        y[(size_t)m * N + n] = __bfloat16_as_ushort(__double2bfloat16(v));
+}
+
+// Outputs (m0 + j, n), j = 0 .. CNT-1 of which the first jn exist, of one
+// thread that holds CNT tokens of output channel n: operands in flight
+// together, B tokens at a time.
+template <bool EPI, int CNT, int B = (CNT < 16 ? CNT : 16)>
+__device__ __forceinline__ void epi_store_tokens(const EpiArgs &e, uint16_t *y, int N, int m0, int jn, int n,
+                                                 const float (&v)[CNT])
+{
+    static_assert(CNT % B == 0, "whole batches");
+    const float bias = epi_bias<EPI>(e, n);
+#pragma unroll
+    for (int j0 = 0; j0 < CNT; j0 += B) {
+        EpiOps o[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (j0 + j < jn)
+                o[j] = epi_load<EPI>(e, m0 + j0 + j, n);
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (j0 + j < jn)
+                epi_store<EPI>(e, y, N, m0 + j0 + j, n, v[j0 + j], bias, o[j]);
+    }
+}
+
+} // namespace wq

@@ -38,6 +38,7 @@
 #include <cudaTypedefs.h>
 
 #include "wq_device.cuh"
+#include "wq_epilogue.cuh"
 #include "wq_gemm_common.cuh"
 #include "wq_internal.h"
 
@@ -51,6 +52,7 @@ struct GemmParams {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
+    EpiArgs epi; // the EPI instances' epilogue
     float *part;   // [S][M][N] fp32 partials (S > 1)
     uint32_t *cnt; // [panels] tickets (S > 1)
 };
@@ -92,17 +94,26 @@ constexpr size_t gemm_smem_bytes()
 // Stores one output row's NT values (token m = column) as y, or as split-K
 // partials followed by the last-arriver reduction.  Runs on the 128
 // dequant/epilogue threads (named barrier 1).
-template <int NT>
+template <int NT, bool EPI>
 __device__ __forceinline__ void gemm_store(const GemmParams &p, int panel, int split, int n, bool nvalid,
                                            float scale, int warp, int lane, uint32_t *s_ticket,
                                            const float (&v)[NT])
 {
     if (p.S == 1) {
         if (nvalid) {
+            const float bias = epi_bias<EPI>(p.epi, n);
 #pragma unroll
-            for (int m = 0; m < NT; ++m)
-                if (m < p.M)
-                    p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[m] * scale));
+            for (int m0 = 0; m0 < NT; m0 += 16) {
+                EpiOps o[16]; // a batch's operands in flight together
+#pragma unroll
+                for (int m = 0; m < 16; ++m)
+                    if (m0 + m < p.M)
+                        o[m] = epi_load<EPI>(p.epi, m0 + m, n);
+#pragma unroll
+                for (int m = 0; m < 16; ++m)
+                    if (m0 + m < p.M)
+                        epi_store<EPI>(p.epi, p.y, p.N, m0 + m, n, v[m0 + m] * scale, bias, o[m]);
+            }
         }
         return;
     }
@@ -120,11 +131,13 @@ __device__ __forceinline__ void gemm_store(const GemmParams &p, int panel, int s
     if (*s_ticket == (uint32_t)(p.S - 1)) {
         __threadfence();
         if (nvalid) {
+            const float bias = epi_bias<EPI>(p.epi, n);
             for (int m = 0; m < p.M; ++m) {
+                const EpiOps o = epi_load<EPI>(p.epi, m, n);
                 float sum = 0.f;
                 for (int s = 0; s < p.S; ++s)
                     sum += __ldcg(&p.part[((size_t)s * p.M + m) * p.N + n]);
-                p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum * scale));
+                epi_store<EPI>(p.epi, p.y, p.N, m, n, sum * scale, bias, o);
             }
         }
         if (warp == 2 && lane == 0)
@@ -132,7 +145,7 @@ __device__ __forceinline__ void gemm_store(const GemmParams &p, int panel, int s
     }
 }
 
-template <int BITS, int NT>
+template <int BITS, int NT, bool EPI>
 __global__ void __launch_bounds__(192, GemmTile<BITS, NT>::kMinBlocks)
     gemm_kernel(const __grid_constant__ CUtensorMap tmx, const GemmParams p)
 {
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(192, GemmTile<BITS, NT>::kMinBlocks)
         const int n = panel * kPanelRows + row;
         const bool nvalid = n < p.N;
         if constexpr (BITS == 4) {
-            gemm_store<NT>(p, panel, split, n, nvalid, 1.f, warp, lane, &s_misc[1], acc);
+            gemm_store<NT, EPI>(p, panel, split, n, nvalid, 1.f, warp, lane, &s_misc[1], acc);
         } else {
             if (!mbar_wait_warp(&accfull[0], 0))
                 ok = false;
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(192, GemmTile<BITS, NT>::kMinBlocks)
                 for (int e = 0; e < 16; ++e)
                     v[c0 + e] = t[e];
             }
-            gemm_store<NT>(p, panel, split, n, nvalid, scale, warp, lane, &s_misc[1], v);
+            gemm_store<NT, EPI>(p, panel, split, n, nvalid, scale, warp, lane, &s_misc[1], v);
         }
     }
 
@@ -392,13 +405,13 @@ __global__ void __launch_bounds__(192, GemmTile<BITS, NT>::kMinBlocks)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <int BITS, int NT>
-static cudaError_t launch_gemm_t(const LinearArgs &a, int S, void *ws, cudaStream_t st)
+template <int BITS, int NT, bool EPI>
+static cudaError_t launch_gemm_e(const LinearArgs &a, int S, void *ws, cudaStream_t st)
 {
     constexpr size_t smem = gemm_smem_bytes<BITS, NT>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
     {
-        const cudaError_t e = kernel_setup((const void *)gemm_kernel<BITS, NT>, smem, 0, 0, nullptr);
+        const cudaError_t e = kernel_setup((const void *)gemm_kernel<BITS, NT, EPI>, smem, 0, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -416,11 +429,18 @@ static cudaError_t launch_gemm_t(const LinearArgs &a, int S, void *ws, cudaStrea
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
+    p.epi = a.epi ? *a.epi : EpiArgs{};
     p.cnt = (uint32_t *)ws;
     p.part = ws ? (float *)((uint8_t *)ws + ws_counter_bytes()) : nullptr;
     dim3 grid(sh.panels(), S);
-    gemm_kernel<BITS, NT><<<grid, 192, smem, st>>>(map, p);
+    gemm_kernel<BITS, NT, EPI><<<grid, 192, smem, st>>>(map, p);
     return cudaGetLastError();
+}
+
+template <int BITS, int NT>
+static cudaError_t launch_gemm_t(const LinearArgs &a, int S, void *ws, cudaStream_t st)
+{
+    return a.epi ? launch_gemm_e<BITS, NT, true>(a, S, ws, st) : launch_gemm_e<BITS, NT, false>(a, S, ws, st);
 }
 
 cudaError_t launch_gemm(const LinearArgs &a, int split, void *ws, int sm_count, cudaStream_t st)

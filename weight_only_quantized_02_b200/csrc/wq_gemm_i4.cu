@@ -59,6 +59,7 @@ struct I4Params {
     const uint16_t *scales; // [P][KB][128] bf16
     const uint8_t *zeros;   // [P][KB][64]: row i at nibble i
     uint16_t *y;
+    EpiArgs epi; // the EPI instances' epilogue
     uint8_t *xd;            // [KB][NR][128] digit blocks
     float *part;            // [G][2 slots][NR/3 tokens][128 rows] fp32
     uint32_t *cnt;          // [panels][4] tickets
@@ -124,7 +125,21 @@ __device__ __forceinline__ void umma_ts_i8(uint32_t d_tmem, uint32_t a_tmem, uin
                  : "memory");
 }
 
-template <int NR>
+// The epilogue operands of output channel n and every token, loaded together;
+// returns the channel's bias.
+template <bool EPI, int MM>
+__device__ __forceinline__ float i4_epi_ops(const I4Params &p, int n, int M, EpiOps (&ops)[MM])
+{
+    if (n >= p.N)
+        return 0.f;
+#pragma unroll
+    for (int m = 0; m < MM; ++m)
+        if (m < M)
+            ops[m] = epi_load<EPI>(p.epi, m, n);
+    return epi_bias<EPI>(p.epi, n);
+}
+
+template <int NR, bool EPI>
 // 14 warps: at most 4 per SM sub-partition, whose register file holds 16K
 // registers, so at most 128 per thread.
 __global__ void __maxnreg__(128) gemm_i4_kernel(const I4Params p)
@@ -395,12 +410,15 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const I4Params p)
                 do {
                     const int lo = max(u0, pnl * KB), hi = min(u1, (pnl + 1) * KB);
                     if (lo == pnl * KB && hi == (pnl + 1) * KB) {
+                        EpiOps ops[MM];
+                        const float bias = i4_epi_ops<EPI, MM>(p, pnl * kPanelRows + row, M, ops);
 #pragma unroll
                         for (int m = 0; m < MM; ++m)
                             if (m < M) // the same across the warp
-                                imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.y, p.K, KB, p.N,
-                                                  pnl * kPanelRows + 32 * quad, m, (double)acc[m] * pow2_of(-s_e[m]),
-                                                  wmax * s_rb[m], lane);
+                                imma_emit_rows<4, EPI>(p.x, p.wq, p.scales, p.zeros, p.epi, p.y, p.K, KB, p.N,
+                                                       pnl * kPanelRows + 32 * quad, m,
+                                                       (double)acc[m] * pow2_of(-s_e[m]), wmax * s_rb[m], bias, ops[m],
+                                                       lane);
                         break;
                     }
                     const int slot = (pnl == sk.first[c]) ? 0 : 1;
@@ -433,12 +451,14 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const I4Params p)
                         for (int m = 0; m < MM; ++m)
                             tot[m] += v[m];
                     }
+                    EpiOps ops[MM];
+                    const float bias = i4_epi_ops<EPI, MM>(p, pnl * kPanelRows + row, M, ops);
 #pragma unroll
                     for (int m = 0; m < MM; ++m)
                         if (m < M) // the same across the warp
-                            imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.y, p.K, KB, p.N,
-                                              pnl * kPanelRows + 32 * quad, m, (double)tot[m] * pow2_of(-s_e[m]),
-                                              wmax * s_rb[m], lane);
+                            imma_emit_rows<4, EPI>(p.x, p.wq, p.scales, p.zeros, p.epi, p.y, p.K, KB, p.N,
+                                                   pnl * kPanelRows + 32 * quad, m, (double)tot[m] * pow2_of(-s_e[m]),
+                                                   wmax * s_rb[m], bias, ops[m], lane);
                     if (lane == 0)
                         atomicExch(&p.cnt[pnl * 4 + quad], 0u);
                 } while (false);
@@ -487,13 +507,13 @@ size_t ws_bytes_gemm_i4(int M, int K, int N)
     return ws_counter_bytes() + KB * NR * 128 + (size_t)kI8MaxCtas * 2 * (NR / 3) * 128 * sizeof(float);
 }
 
-template <int NR>
-static cudaError_t launch_i4_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+template <int NR, bool EPI>
+static cudaError_t launch_i4_e(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
 {
     constexpr size_t smem = i4_smem_bytes<NR>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
     {
-        const cudaError_t e = kernel_setup((const void *)gemm_i4_kernel<NR>, smem, 0, 0, nullptr);
+        const cudaError_t e = kernel_setup((const void *)gemm_i4_kernel<NR, EPI>, smem, 0, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -509,6 +529,7 @@ static cudaError_t launch_i4_t(const LinearArgs &a, void *ws, int sm_count, cuda
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
+    p.epi = a.epi ? *a.epi : EpiArgs{};
     p.cnt = (uint32_t *)ws;
     p.grid = p.cnt + ws_grid_counter();
     p.res = reinterpret_cast<unsigned long long *>(p.cnt + ws_res_counter());
@@ -528,7 +549,13 @@ static cudaError_t launch_i4_t(const LinearArgs &a, void *ws, int sm_count, cuda
     cfg.gridDim = dim3(G);
     cfg.blockDim = dim3(kI4Threads);
     cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelEx(&cfg, gemm_i4_kernel<NR>, p);
+    return cudaLaunchKernelEx(&cfg, gemm_i4_kernel<NR, EPI>, p);
+}
+
+template <int NR>
+static cudaError_t launch_i4_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+{
+    return a.epi ? launch_i4_e<NR, true>(a, ws, sm_count, st) : launch_i4_e<NR, false>(a, ws, sm_count, st);
 }
 
 cudaError_t launch_gemm_i4(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)

@@ -67,6 +67,7 @@ struct I8Params {
     const uint8_t *wq;
     const uint16_t *scales;
     uint16_t *y;
+    EpiArgs epi; // the EPI instances' epilogue
     uint8_t *xd;    // [KB][NR][128] digit blocks
     int32_t *part;  // [G][2 slots][NR][128 rows] int32
     uint32_t *cnt;  // [panels][4] tickets
@@ -104,7 +105,21 @@ constexpr size_t i8_smem_bytes()
            2 * kI8MaxM * 4 + kI8MaxM * 8 + (size_t)2 * (2 * kI8MaxCtas + 1) * 4;
 }
 
-template <int NR>
+// The epilogue operands of output channel n and tokens m0 .. m0 + CNT - 1,
+// loaded together; returns the channel's bias.
+template <bool EPI, int CNT>
+__device__ __forceinline__ float i8_epi_ops(const I8Params &p, int n, int m0, int M, EpiOps (&ops)[CNT])
+{
+    if (n >= p.N)
+        return 0.f;
+#pragma unroll
+    for (int t = 0; t < CNT; ++t)
+        if (m0 + t < M)
+            ops[t] = epi_load<EPI>(p.epi, m0 + t, n);
+    return epi_bias<EPI>(p.epi, n);
+}
+
+template <int NR, bool EPI>
 __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(const I8Params p)
 {
     using C = I8Cfg<NR>;
@@ -317,13 +332,15 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
                         for (int j = 0; j < CG; ++j)
                             v[j] += pre[j];
                     }
+                    EpiOps ops[CG / 3];
+                    const float bias = i8_epi_ops<EPI, CG / 3>(p, pnl * kPanelRows + row, c0 / 3, M, ops);
 #pragma unroll
                     for (int t = 0; t < CG / 3; ++t) {
                         const int m = c0 / 3 + t; // the same across the warp
                         if (m < M)
-                            imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, p.y, K, KB, p.N, pnl * kPanelRows + 32 * quad,
+                            imma_emit_rows<8, EPI>(p.x, p.wq, p.scales, nullptr, p.epi, p.y, K, KB, p.N, pnl * kPanelRows + 32 * quad,
                                               m, i8_value(v[3 * t], v[3 * t + 1], v[3 * t + 2], s_n * pow2_of(-s_e[m])),
-                                              128.0 * s_n * s_rb[m], lane);
+                                              128.0 * s_n * s_rb[m], bias, ops[t], lane);
                     }
                 } else {
 #pragma unroll
@@ -366,13 +383,15 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
                     for (int j = 0; j < CG; ++j)
                         tot[j] += v[j];
                 }
+                EpiOps ops[CG / 3];
+                const float bias = i8_epi_ops<EPI, CG / 3>(p, pnl * kPanelRows + row, c0 / 3, M, ops);
 #pragma unroll
                 for (int t = 0; t < CG / 3; ++t) {
                     const int m = c0 / 3 + t; // the same across the warp
                     if (m < M)
-                        imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, p.y, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
+                        imma_emit_rows<8, EPI>(p.x, p.wq, p.scales, nullptr, p.epi, p.y, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
                                           i8_value(tot[3 * t], tot[3 * t + 1], tot[3 * t + 2], s_n * pow2_of(-s_e[m])),
-                                          128.0 * s_n * s_rb[m], lane);
+                                          128.0 * s_n * s_rb[m], bias, ops[t], lane);
                 }
             }
             if (lane == 0)
@@ -417,14 +436,14 @@ size_t ws_bytes_gemm_i8(int M, int K, int N)
     return ws_counter_bytes() + KB * NR * 128 + ctas * 2 * NR * 128 * sizeof(int32_t);
 }
 
-template <int NR>
-static cudaError_t launch_i8_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+template <int NR, bool EPI>
+static cudaError_t launch_i8_e(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
 {
     constexpr size_t smem = i8_smem_bytes<NR>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
     static_assert(I8Cfg<NR>::kOcc == 1 || 2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
     {
-        const cudaError_t e = kernel_setup((const void *)gemm_i8_kernel<NR>, smem, 0, 0, nullptr);
+        const cudaError_t e = kernel_setup((const void *)gemm_i8_kernel<NR, EPI>, smem, 0, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -439,6 +458,7 @@ static cudaError_t launch_i8_t(const LinearArgs &a, void *ws, int sm_count, cuda
     p.wq = (const uint8_t *)a.wq;
     p.scales = (const uint16_t *)a.scales;
     p.y = a.y;
+    p.epi = a.epi ? *a.epi : EpiArgs{};
     p.cnt = (uint32_t *)ws;
     p.grid = p.cnt + ws_grid_counter();
     p.res = reinterpret_cast<unsigned long long *>(p.cnt + ws_res_counter());
@@ -461,7 +481,13 @@ static cudaError_t launch_i8_t(const LinearArgs &a, void *ws, int sm_count, cuda
     cfg.gridDim = dim3(G);
     cfg.blockDim = dim3(kI8Threads);
     cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<NR>, p);
+    return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<NR, EPI>, p);
+}
+
+template <int NR>
+static cudaError_t launch_i8_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+{
+    return a.epi ? launch_i8_e<NR, true>(a, ws, sm_count, st) : launch_i8_e<NR, false>(a, ws, sm_count, st);
 }
 
 cudaError_t launch_gemm_i8(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)

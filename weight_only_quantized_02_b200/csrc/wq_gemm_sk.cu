@@ -32,6 +32,7 @@
 #include <cstdint>
 
 #include "wq_device.cuh"
+#include "wq_epilogue.cuh"
 #include "wq_gemm_common.cuh"
 #include "wq_internal.h"
 
@@ -45,6 +46,7 @@ struct GemmSkParams {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
+    EpiArgs epi; // the EPI instances' epilogue
     float *part;   // [CTAs][2][128 rows][NT]
     uint32_t *cnt; // [panels][8]
 };
@@ -99,7 +101,7 @@ __device__ __forceinline__ void tmem_load_cols(uint32_t taddr, float (&v)[HALF])
     tmem_wait_ld();
 }
 
-template <int BITS, int NT>
+template <int BITS, int NT, bool EPI>
 __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kMaxRegs))
     gemm_sk_kernel(const __grid_constant__ CUtensorMap tmx, const GemmSkParams p)
 {
@@ -262,11 +264,20 @@ __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kM
                 scale = nrow < p.N ? bf16_bits_to_float(p.scales[nrow]) : 0.f;
             auto store_y = [&](const float (&t)[HALF]) {
                 if (nrow < p.N) {
+                    const float bias = epi_bias<EPI>(p.epi, nrow);
+                    constexpr int B = HALF < 16 ? HALF : 16; // a batch's operands in flight together
 #pragma unroll
-                    for (int c = 0; c < HALF; ++c)
-                        if (h * HALF + c < p.M)
-                            p.y[(size_t)(h * HALF + c) * p.N + nrow] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(t[c] * scale));
+                    for (int c0 = 0; c0 < HALF; c0 += B) {
+                        EpiOps o[B];
+#pragma unroll
+                        for (int c = 0; c < B; ++c)
+                            if (h * HALF + c0 + c < p.M)
+                                o[c] = epi_load<EPI>(p.epi, h * HALF + c0 + c, nrow);
+#pragma unroll
+                        for (int c = 0; c < B; ++c)
+                            if (h * HALF + c0 + c < p.M)
+                                epi_store<EPI>(p.epi, p.y, p.N, h * HALF + c0 + c, nrow, t[c0 + c] * scale, bias, o[c]);
+                    }
                 }
             };
             if (lo == pnl * KB && hi == (pnl + 1) * KB) {
@@ -323,11 +334,16 @@ __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kM
                     }
                 }
                 if (nrow < p.N) {
+                    const float bias = epi_bias<EPI>(p.epi, nrow);
+                    EpiOps o[CH];
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
                         if (h * HALF + c0 + c < p.M)
-                            p.y[(size_t)(h * HALF + c0 + c) * p.N + nrow] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(tot[c] * scale));
+                            o[c] = epi_load<EPI>(p.epi, h * HALF + c0 + c, nrow);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        if (h * HALF + c0 + c < p.M)
+                            epi_store<EPI>(p.epi, p.y, p.N, h * HALF + c0 + c, nrow, tot[c] * scale, bias, o[c]);
                 }
             }
             if (lane == 0)
@@ -465,14 +481,14 @@ __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kM
     }
 }
 
-template <int BITS, int NT>
-static cudaError_t launch_gemm_sk_t(const LinearArgs &a, int ctas_per_sm, void *ws, int sm_count, cudaStream_t st)
+template <int BITS, int NT, bool EPI>
+static cudaError_t launch_gemm_sk_e(const LinearArgs &a, int ctas_per_sm, void *ws, int sm_count, cudaStream_t st)
 {
     using C = GskCfg<BITS, NT>;
     constexpr size_t smem = gemm_sk_smem_bytes<BITS, NT>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
     {
-        const cudaError_t e = kernel_setup((const void *)gemm_sk_kernel<BITS, NT>, smem, 0, 0, nullptr);
+        const cudaError_t e = kernel_setup((const void *)gemm_sk_kernel<BITS, NT, EPI>, smem, 0, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -490,6 +506,7 @@ static cudaError_t launch_gemm_sk_t(const LinearArgs &a, int ctas_per_sm, void *
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
+    p.epi = a.epi ? *a.epi : EpiArgs{};
     p.cnt = (uint32_t *)ws;
     p.part = (float *)((uint8_t *)ws + ws_counter_bytes());
     const int per_sm = (ctas_per_sm >= 1 && ctas_per_sm < C::kOcc) ? ctas_per_sm : C::kOcc;
@@ -508,7 +525,14 @@ static cudaError_t launch_gemm_sk_t(const LinearArgs &a, int ctas_per_sm, void *
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_sk_kernel<BITS, NT>, map, p);
+    return cudaLaunchKernelEx(&cfg, gemm_sk_kernel<BITS, NT, EPI>, map, p);
+}
+
+template <int BITS, int NT>
+static cudaError_t launch_gemm_sk_t(const LinearArgs &a, int ctas_per_sm, void *ws, int sm_count, cudaStream_t st)
+{
+    return a.epi ? launch_gemm_sk_e<BITS, NT, true>(a, ctas_per_sm, ws, sm_count, st)
+                 : launch_gemm_sk_e<BITS, NT, false>(a, ctas_per_sm, ws, sm_count, st);
 }
 
 cudaError_t launch_gemm_sk(const LinearArgs &a, int ctas_per_sm, void *ws, int sm_count, cudaStream_t st)

@@ -49,6 +49,7 @@
 #include <cuda_bf16.h>
 
 #include "wq_device.cuh"
+#include "wq_epilogue.cuh"
 #include "wq_gemm_common.cuh"
 #include "wq_internal.h"
 
@@ -62,6 +63,7 @@ struct GemmW4Params {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
+    EpiArgs epi; // the EPI instances' epilogue
     float *part;   // [CTAs][2 slots][NT tokens][128 rows]
     uint32_t *cnt; // [panels][8] tickets
 };
@@ -135,7 +137,7 @@ constexpr size_t gemm_w4_smem_bytes()
 // 128-byte row segment per warp; CG contributors x 16 tokens are in flight
 // together (this runs at the very end of the call, on its critical path).
 // Called after the retire loop, whose register totals are dead by then.
-template <int NT, int CW>
+template <int NT, int CW, bool EPI>
 __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &sk, int pnl, int cf, int cl, int r,
                                          int t0)
 {
@@ -168,18 +170,12 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
         }
         if (nrow < p.N) {
             const int jn = min(16, p.M - t0 - j0);
-            uint16_t *yp = p.y + (size_t)(t0 + j0) * p.N + nrow;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (j < jn)
-                    *yp = __bfloat16_as_ushort(__float2bfloat16_rn(acc[j]));
-                yp += p.N;
-            }
+            epi_store_tokens<EPI, 16>(p.epi, p.y, p.N, t0 + j0, jn, nrow, acc);
         }
     }
 }
 
-template <int NT>
+template <int NT, bool EPI>
 __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const __grid_constant__ CUtensorMap tmx,
                                                                 const GemmW4Params p)
 {
@@ -334,13 +330,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const _
             if (lo == pnl * KB && hi == (pnl + 1) * KB) {
                 if (nrow < p.N) {
                     const int jn = min(CW, p.M - t0); // tokens of this slice that exist
-                    uint16_t *yp = p.y + (size_t)t0 * p.N + nrow;
-#pragma unroll
-                    for (int j = 0; j < CW; ++j) {
-                        if (j < jn)
-                            *yp = __bfloat16_as_ushort(__float2bfloat16_rn(tot[j]));
-                        yp += p.N;
-                    }
+                    epi_store_tokens<EPI, CW>(p.epi, p.y, p.N, t0, jn, nrow, tot);
                 }
                 return;
             }
@@ -407,7 +397,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const _
         }
         __syncwarp(); // lane 0's acquire (the tickets) orders every lane's reads below
         for (int f = 0; f < nfix && ok; ++f) {
-            w4_fixup<NT, CW>(p, sk, fix_pnl[f], fix_cf[f], fix_cl[f], r, c * CW);
+            w4_fixup<NT, CW, EPI>(p, sk, fix_pnl[f], fix_cf[f], fix_cl[f], r, c * CW);
             if (lane == 0)
                 atomicExch(&p.cnt[fix_pnl[f] * 8 + dw], 0u); // ready for the next call
         }
@@ -495,13 +485,13 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const _
     }
 }
 
-template <int NT>
-static cudaError_t launch_gemm_w4_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+template <int NT, bool EPI>
+static cudaError_t launch_gemm_w4_e(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
 {
     constexpr size_t smem = gemm_w4_smem_bytes<NT>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
     {
-        const cudaError_t e = kernel_setup((const void *)gemm_w4_kernel<NT>, smem, 0, 0, nullptr);
+        const cudaError_t e = kernel_setup((const void *)gemm_w4_kernel<NT, EPI>, smem, 0, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -519,6 +509,7 @@ static cudaError_t launch_gemm_w4_t(const LinearArgs &a, void *ws, int sm_count,
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
+    p.epi = a.epi ? *a.epi : EpiArgs{};
     p.cnt = (uint32_t *)ws;
     p.part = (float *)((uint8_t *)ws + ws_counter_bytes());
     int G = sm_count;
@@ -536,7 +527,13 @@ static cudaError_t launch_gemm_w4_t(const LinearArgs &a, void *ws, int sm_count,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_w4_kernel<NT>, map, p);
+    return cudaLaunchKernelEx(&cfg, gemm_w4_kernel<NT, EPI>, map, p);
+}
+
+template <int NT>
+static cudaError_t launch_gemm_w4_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+{
+    return a.epi ? launch_gemm_w4_e<NT, true>(a, ws, sm_count, st) : launch_gemm_w4_e<NT, false>(a, ws, sm_count, st);
 }
 
 cudaError_t launch_gemm_w4(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)

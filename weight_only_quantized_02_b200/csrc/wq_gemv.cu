@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 
 #include "wq_device.cuh"
+#include "wq_epilogue.cuh"
 #include "wq_internal.h"
 
 namespace wq {
@@ -27,6 +28,7 @@ struct GemvParams {
     const uint8_t *zeros;
     uint16_t *y;
     Shape sh;
+    EpiArgs epi; // the EPI instances' epilogue
     int ks; // K slices per 16-row block (1, 2, 4, 8); the 8 warps of a CTA
             // cover 8/ks row blocks
 };
@@ -80,13 +82,6 @@ struct Act {
         } else {
             return s8pair_bf16(u, h);
         }
-    }
-    __device__ static __forceinline__ uint16_t out(float v)
-    {
-        if constexpr (F16)
-            return __half_as_ushort(__float2half_rn(v));
-        else
-            return __bfloat16_as_ushort(__float2bfloat16_rn(v));
     }
 };
 
@@ -348,7 +343,7 @@ __device__ __forceinline__ void gemv_int4_slice(const GemvParams &p, int rb, int
     }
 }
 
-template <int BITS, int MT, int LG = 128, bool F16 = false>
+template <int BITS, int MT, int LG, bool F16, bool EPI>
 __global__ void __launch_bounds__(kGemvWarps * 32) gemv_kernel(const GemvParams p)
 {
     __shared__ float red[kGemvWarps][MT * 4][32];
@@ -404,28 +399,38 @@ __global__ void __launch_bounds__(kGemvWarps * 32) gemv_kernel(const GemvParams 
                 s_lo = bf16_bits_to_float(__ldg(p.scales + n_lo));
                 s_hi = bf16_bits_to_float(__ldg(p.scales + n_hi));
             }
+            const float b_lo = epi_bias<EPI, F16>(p.epi, n_lo), b_hi = epi_bias<EPI, F16>(p.epi, n_hi);
+            EpiOps o_lo[MT][2], o_hi[MT][2]; // every operand in flight together
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int m0 = 8 * mt + 2 * t, m1 = m0 + 1;
-                if (m0 < p.M) {
-                    p.y[(size_t)m0 * p.N + n_lo] = Act<F16>::out(acc[mt][0] * s_lo);
-                    p.y[(size_t)m0 * p.N + n_hi] = Act<F16>::out(acc[mt][2] * s_hi);
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int m = 8 * mt + 2 * t + e;
+                    if (m < p.M) {
+                        o_lo[mt][e] = epi_load<EPI, F16>(p.epi, m, n_lo);
+                        o_hi[mt][e] = epi_load<EPI, F16>(p.epi, m, n_hi);
+                    }
                 }
-                if (m1 < p.M) {
-                    p.y[(size_t)m1 * p.N + n_lo] = Act<F16>::out(acc[mt][1] * s_lo);
-                    p.y[(size_t)m1 * p.N + n_hi] = Act<F16>::out(acc[mt][3] * s_hi);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int m = 8 * mt + 2 * t + e;
+                    if (m < p.M) {
+                        epi_store<EPI, F16>(p.epi, p.y, p.N, m, n_lo, acc[mt][e] * s_lo, b_lo, o_lo[mt][e]);
+                        epi_store<EPI, F16>(p.epi, p.y, p.N, m, n_hi, acc[mt][2 + e] * s_hi, b_hi, o_hi[mt][e]);
+                    }
                 }
-            }
         }
     }
 }
 
-template <int BITS, int MT, int LG = 128, bool F16 = false>
+template <int BITS, int MT, int LG, bool F16, bool EPI>
 static cudaError_t launch_gemv_t(const GemvParams &p, int sm_count, cudaStream_t st)
 {
     int occ = 1; // CTAs per SM, from the hardware occupancy query (cached per device)
     {
-        const cudaError_t e = kernel_setup((const void *)gemv_kernel<BITS, MT, LG, F16>, 0, kGemvWarps * 32, 0, &occ);
+        const cudaError_t e = kernel_setup((const void *)gemv_kernel<BITS, MT, LG, F16, EPI>, 0, kGemvWarps * 32, 0, &occ);
         if (e != cudaSuccess)
             return e;
     }
@@ -443,31 +448,31 @@ static cudaError_t launch_gemv_t(const GemvParams &p, int sm_count, cudaStream_t
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kGemvWarps * 32);
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, gemv_kernel<BITS, MT, LG, F16>, p);
+    return cudaLaunchKernelEx(&cfg, gemv_kernel<BITS, MT, LG, F16, EPI>, p);
 }
 
-template <bool F16>
+template <bool F16, bool EPI>
 static cudaError_t launch_gemv_fmt(const GemvParams &p, int bits, int group, int sm_count, cudaStream_t st)
 {
     const int mt = (p.M + 7) / 8;
     if (bits == 8) {
-        if (mt == 1) return launch_gemv_t<8, 1, 128, F16>(p, sm_count, st);
-        if (mt == 2) return launch_gemv_t<8, 2, 128, F16>(p, sm_count, st);
-        return launch_gemv_t<8, 4, 128, F16>(p, sm_count, st);
+        if (mt == 1) return launch_gemv_t<8, 1, 128, F16, EPI>(p, sm_count, st);
+        if (mt == 2) return launch_gemv_t<8, 2, 128, F16, EPI>(p, sm_count, st);
+        return launch_gemv_t<8, 4, 128, F16, EPI>(p, sm_count, st);
     }
     if (group == 32) {
-        if (mt == 1) return launch_gemv_t<4, 1, 32, F16>(p, sm_count, st);
-        if (mt == 2) return launch_gemv_t<4, 2, 32, F16>(p, sm_count, st);
-        return launch_gemv_t<4, 4, 32, F16>(p, sm_count, st);
+        if (mt == 1) return launch_gemv_t<4, 1, 32, F16, EPI>(p, sm_count, st);
+        if (mt == 2) return launch_gemv_t<4, 2, 32, F16, EPI>(p, sm_count, st);
+        return launch_gemv_t<4, 4, 32, F16, EPI>(p, sm_count, st);
     }
     if (group == 64) {
-        if (mt == 1) return launch_gemv_t<4, 1, 64, F16>(p, sm_count, st);
-        if (mt == 2) return launch_gemv_t<4, 2, 64, F16>(p, sm_count, st);
-        return launch_gemv_t<4, 4, 64, F16>(p, sm_count, st);
+        if (mt == 1) return launch_gemv_t<4, 1, 64, F16, EPI>(p, sm_count, st);
+        if (mt == 2) return launch_gemv_t<4, 2, 64, F16, EPI>(p, sm_count, st);
+        return launch_gemv_t<4, 4, 64, F16, EPI>(p, sm_count, st);
     }
-    if (mt == 1) return launch_gemv_t<4, 1, 128, F16>(p, sm_count, st);
-    if (mt == 2) return launch_gemv_t<4, 2, 128, F16>(p, sm_count, st);
-    return launch_gemv_t<4, 4, 128, F16>(p, sm_count, st);
+    if (mt == 1) return launch_gemv_t<4, 1, 128, F16, EPI>(p, sm_count, st);
+    if (mt == 2) return launch_gemv_t<4, 2, 128, F16, EPI>(p, sm_count, st);
+    return launch_gemv_t<4, 4, 128, F16, EPI>(p, sm_count, st);
 }
 
 cudaError_t launch_gemv(const LinearArgs &a, int ks, int sm_count, cudaStream_t st, bool f16)
@@ -483,8 +488,14 @@ cudaError_t launch_gemv(const LinearArgs &a, int ks, int sm_count, cudaStream_t 
     p.y = a.y;
     p.sh = Shape{a.bits, a.K, a.N, a.group};
     p.ks = ks;
-    return f16 ? launch_gemv_fmt<true>(p, a.bits, a.group, sm_count, st)
-               : launch_gemv_fmt<false>(p, a.bits, a.group, sm_count, st);
+    if (a.epi) {
+        p.epi = *a.epi;
+        return f16 ? launch_gemv_fmt<true, true>(p, a.bits, a.group, sm_count, st)
+                   : launch_gemv_fmt<false, true>(p, a.bits, a.group, sm_count, st);
+    }
+    p.epi = EpiArgs{};
+    return f16 ? launch_gemv_fmt<true, false>(p, a.bits, a.group, sm_count, st)
+               : launch_gemv_fmt<false, false>(p, a.bits, a.group, sm_count, st);
 }
 
 } // namespace wq

@@ -61,6 +61,7 @@ struct GiParams {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
+    EpiArgs epi; // the EPI instances' epilogue
     uint32_t *part; // [kGiMaxWarps][2 slots][16 rows][NR] partials
     uint32_t *cnt;  // one ticket per 16-row block
     const uint32_t *wmax; // INT4: max |s (q - z)| over the whole weight (binary32 bits, packed trailer)
@@ -313,7 +314,7 @@ __host__ __device__ __forceinline__ bool gi_contrib_at(const GiParams &p, int G,
 // n0 + r): value(q) is the integer path's y in binary64.  The exactness
 // guard (wq_imma.cuh) vouches for it or the warp recomputes that output in
 // binary64 from x and the packed codes.  All 32 lanes call it together.
-template <int BITS, class Value>
+template <int BITS, bool EPI, class Value>
 __device__ __forceinline__ void gi_emit(const GiParams &p, int n0, const int *s_e, const unsigned long long *s_res,
                                         Value value, int lane)
 {
@@ -322,13 +323,17 @@ __device__ __forceinline__ void gi_emit(const GiParams &p, int n0, const int *s_
     for (int q0 = 0; q0 < 16 * M; q0 += 32) {
         const int q = q0 + lane, r = q & 15, m = q >> 4;
         bool redo = false;
+        float bias = 0.f;
+        EpiOps o{1.f, 0.f};
         if (q < 16 * M) {
+            o = epi_load<EPI>(p.epi, m, n0 + r);
+            bias = epi_bias<EPI>(p.epi, n0 + r);
             const double v = value(q);
             const double wmax =
                 BITS == 8 ? 128.0 * (double)bf16_bits_to_float(p.scales[n0 + r]) : (double)wmax4;
             redo = !exact_enough(v, wmax * residual_bound(s_res[m], s_e[m]));
             if (!redo)
-                p.y[(size_t)m * N + n0 + r] = __bfloat16_as_ushort(__double2bfloat16(v));
+                epi_store64<EPI>(p.epi, p.y, N, m, n0 + r, v, bias, o);
         }
         for (uint32_t mask = __ballot_sync(0xffffffffu, redo); mask; mask &= mask - 1) {
             const int src = __ffs(mask) - 1, qq = q0 + src, rr = qq & 15, mm = qq >> 4;
@@ -336,19 +341,19 @@ __device__ __forceinline__ void gi_emit(const GiParams &p, int n0, const int *s_
             if constexpr (BITS == 8)
                 v *= (double)bf16_bits_to_float(p.scales[n0 + rr]);
             if (lane == src)
-                p.y[(size_t)mm * N + n0 + rr] = __bfloat16_as_ushort(__double2bfloat16(v));
+                epi_store64<EPI>(p.epi, p.y, N, mm, n0 + rr, v, bias, o);
         }
     }
 }
 
 // One segment's output, its accumulators in red ([16 rows][NR]; INT8 int32
 // digit sums D_i, INT4 fp32 group-scaled sums A_i): y of the 16 x M outputs.
-template <int BITS, int NR>
+template <int BITS, int NR, bool EPI>
 __device__ __forceinline__ void gi_write_y(const GiParams &p, int rb, const uint32_t *red, const int *s_e,
                                            const unsigned long long *s_res, int lane)
 {
     const int n0 = 16 * rb;
-    gi_emit<BITS>(
+    gi_emit<BITS, EPI>(
         p, n0, s_e, s_res,
         [&](int q) -> double {
             const int r = q & 15, m = q >> 4;
@@ -398,7 +403,7 @@ __device__ __forceinline__ uint32_t gi_shared_partial(const GiParams &p, int rb,
 // partials in order (up to four loaded per round trip to L2) and writes y.
 // Its ticket's acquire (taken earlier in program order) orders the reads.
 // list: this warp's scratch of at least CPR words (partial offsets).
-template <int BITS, int NT, int WARPS>
+template <int BITS, int NT, int WARPS, bool EPI>
 __device__ __forceinline__ void gi_shared_fixup(const GiParams &p, int rb, uint32_t ticket, int G, const int *s_e,
                                                 const unsigned long long *s_res, uint32_t *list, int lane)
 {
@@ -422,7 +427,7 @@ __device__ __forceinline__ void gi_shared_fixup(const GiParams &p, int rb, uint3
     __syncwarp();
     if (ticket != (uint32_t)(nc - 1))
         return;
-    gi_emit<BITS>(
+    gi_emit<BITS, EPI>(
         p, n0, s_e, s_res,
         [&](int q) -> double {
             const int r = q & 15, m = q >> 4;
@@ -477,7 +482,7 @@ __device__ __forceinline__ void gi_shared_fixup(const GiParams &p, int rb, uint3
 // blocks that were split between its warps, summed from the stash in warp
 // order (INT8: exact integers; INT4: each contributor's value in binary64,
 // summed in binary64) and written to y.
-template <int BITS, int NT, int WARPS>
+template <int BITS, int NT, int WARPS, bool EPI>
 __device__ __forceinline__ void gi_local_out(const GiParams &p, const GiCta &ct, int c, const uint32_t *stash,
                                              const int *s_e, const unsigned long long *s_res, int warp, int lane)
 {
@@ -489,7 +494,7 @@ __device__ __forceinline__ void gi_local_out(const GiParams &p, const GiCta &ct,
         if (wf == wl)
             continue; // one warp had it whole and wrote y
         const int n0 = 16 * (c * p.LB + j);
-        gi_emit<BITS>(
+        gi_emit<BITS, EPI>(
             p, n0, s_e, s_res,
             [&](int q) -> double {
                 const int r = q & 15, m = q >> 4;
@@ -519,7 +524,7 @@ __device__ __forceinline__ void gi_local_out(const GiParams &p, const GiCta &ct,
 
 // WARPS = 16: one CTA per SM (the digit rows made once per SM); WARPS = 8:
 // two per SM.  Either way 128 registers per thread and 16 warps per SM.
-template <int BITS, int NT, int WARPS>
+template <int BITS, int NT, int WARPS, bool EPI>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_i8_kernel(const GiParams p)
 {
     constexpr int NR = 8 * NT;
@@ -761,7 +766,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_i8_kernel(const G
                 ++npend;
             } else if (whole) {
                 __syncwarp();
-                gi_write_y<BITS, NR>(p, crb, red, s_e, s_res, lane);
+                gi_write_y<BITS, NR, EPI>(p, crb, red, s_e, s_res, lane);
                 __syncwarp(); // red is rewritten by the next segment
             }
             ++crb;
@@ -772,11 +777,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_i8_kernel(const G
         }
     }
     if (npend > 0)
-        gi_shared_fixup<BITS, NT, WARPS>(p, pend_rb0, pend_t0, G, s_e, s_res, st0, lane);
+        gi_shared_fixup<BITS, NT, WARPS, EPI>(p, pend_rb0, pend_t0, G, s_e, s_res, st0, lane);
     if (npend > 1)
-        gi_shared_fixup<BITS, NT, WARPS>(p, pend_rb1, pend_t1, G, s_e, s_res, st0, lane);
+        gi_shared_fixup<BITS, NT, WARPS, EPI>(p, pend_rb1, pend_t1, G, s_e, s_res, st0, lane);
     __syncthreads(); // every warp's stash is complete
-    gi_local_out<BITS, NT, WARPS>(p, ct, c, stash, s_e, s_res, warp, lane);
+    gi_local_out<BITS, NT, WARPS, EPI>(p, ct, c, stash, s_e, s_res, warp, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -824,14 +829,14 @@ static bool gi_plan(GiParams &p, int bits, int K, int N, int G, int warps)
     return (long long)NRB * p.CPR * warps < (1LL << 31) && (long long)p.RL * G < (1LL << 31);
 }
 
-template <int BITS, int NT, int WARPS>
+template <int BITS, int NT, int WARPS, bool EPI>
 static cudaError_t launch_gi_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
 {
     const int smem = (int)gi_smem_bytes_w(BITS, a.M, a.K, WARPS);
     int occ = 1;
     {
         const cudaError_t e =
-            kernel_setup((const void *)gemv_i8_kernel<BITS, NT, WARPS>, kGiMaxSmem, WARPS * 32, smem, &occ);
+            kernel_setup((const void *)gemv_i8_kernel<BITS, NT, WARPS, EPI>, kGiMaxSmem, WARPS * 32, smem, &occ);
         if (e != cudaSuccess)
             return e;
     }
@@ -849,6 +854,7 @@ static cudaError_t launch_gi_t(const LinearArgs &a, void *ws, int sm_count, cuda
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
+    p.epi = a.epi ? *a.epi : EpiArgs{};
     p.cnt = (uint32_t *)ws;
     p.part = (uint32_t *)((uint8_t *)ws + ws_counter_bytes());
     p.wmax = trailer_wmax(a.wq, sh);
@@ -872,13 +878,17 @@ static cudaError_t launch_gi_t(const LinearArgs &a, void *ws, int sm_count, cuda
     cfg.gridDim = dim3(G);
     cfg.blockDim = dim3(WARPS * 32);
     cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelEx(&cfg, gemv_i8_kernel<BITS, NT, WARPS>, p);
+    return cudaLaunchKernelEx(&cfg, gemv_i8_kernel<BITS, NT, WARPS, EPI>, p);
 }
 
 template <int BITS, int NT>
 static cudaError_t launch_gi_w(const LinearArgs &a, int split, void *ws, int sm_count, cudaStream_t st)
 {
-    return split == 2 ? launch_gi_t<BITS, NT, 8>(a, ws, sm_count, st) : launch_gi_t<BITS, NT, 16>(a, ws, sm_count, st);
+    if (a.epi)
+        return split == 2 ? launch_gi_t<BITS, NT, 8, true>(a, ws, sm_count, st)
+                          : launch_gi_t<BITS, NT, 16, true>(a, ws, sm_count, st);
+    return split == 2 ? launch_gi_t<BITS, NT, 8, false>(a, ws, sm_count, st)
+                      : launch_gi_t<BITS, NT, 16, false>(a, ws, sm_count, st);
 }
 
 cudaError_t launch_gemv_i8(const LinearArgs &a, int split, void *ws, int sm_count, cudaStream_t st)

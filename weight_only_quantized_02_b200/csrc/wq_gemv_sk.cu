@@ -24,6 +24,7 @@
 #include <mutex>
 
 #include "wq_device.cuh"
+#include "wq_epilogue.cuh"
 #include "wq_internal.h"
 
 namespace wq {
@@ -37,6 +38,7 @@ struct GemvSkParams {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
+    EpiArgs epi; // the EPI instances' epilogue
     int KB, U; // k-blocks per panel, units = panels * KB
     float *part;
     uint32_t *cnt;
@@ -143,7 +145,7 @@ __device__ __forceinline__ void sk_int4_tile(const uint4 &w, const uint8_t *xs, 
 }
 
 // OCC = CTAs per SM the instance is built for (register bound and ring depth).
-template <int BITS, int MT, int OCC>
+template <int BITS, int MT, int OCC, bool EPI>
 __global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const GemvSkParams p)
 {
     using C = SkCfg<BITS, MT, OCC>;
@@ -245,21 +247,33 @@ __global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const GemvSkPa
                 s_hi = n_hi < p.N ? bf16_bits_to_float(p.scales[n_hi]) : 0.f;
             }
             auto store_y = [&](const float (&v)[MT][4]) {
+                const float b_lo = n_lo < p.N ? epi_bias<EPI>(p.epi, n_lo) : 0.f;
+                const float b_hi = n_hi < p.N ? epi_bias<EPI>(p.epi, n_hi) : 0.f;
+                EpiOps o_lo[MT][2], o_hi[MT][2]; // every operand in flight together
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const int m0 = 8 * mt + 2 * t;
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (m0 + e < p.M) {
+                        const int m = 8 * mt + 2 * t + e;
+                        if (m < p.M) {
                             if (n_lo < p.N)
-                                p.y[(size_t)(m0 + e) * p.N + n_lo] =
-                                    __bfloat16_as_ushort(__float2bfloat16_rn(v[mt][e] * s_lo));
+                                o_lo[mt][e] = epi_load<EPI>(p.epi, m, n_lo);
                             if (n_hi < p.N)
-                                p.y[(size_t)(m0 + e) * p.N + n_hi] =
-                                    __bfloat16_as_ushort(__float2bfloat16_rn(v[mt][2 + e] * s_hi));
+                                o_hi[mt][e] = epi_load<EPI>(p.epi, m, n_hi);
                         }
                     }
-                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int m = 8 * mt + 2 * t + e;
+                        if (m < p.M) {
+                            if (n_lo < p.N)
+                                epi_store<EPI>(p.epi, p.y, p.N, m, n_lo, v[mt][e] * s_lo, b_lo, o_lo[mt][e]);
+                            if (n_hi < p.N)
+                                epi_store<EPI>(p.epi, p.y, p.N, m, n_hi, v[mt][2 + e] * s_hi, b_hi, o_hi[mt][e]);
+                        }
+                    }
             };
             if (lo == pnl * KB && hi == (pnl + 1) * KB) {
                 store_y(acc);
@@ -404,14 +418,14 @@ __global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const GemvSkPa
         atomicExch(&g_gemv_sk_error, kErrTimeout);
 }
 
-template <int BITS, int MT, int OCC>
+template <int BITS, int MT, int OCC, bool EPI>
 static cudaError_t launch_sk_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
 {
     using C = SkCfg<BITS, MT, OCC>;
     constexpr size_t smem = 128 + (size_t)C::kStages * C::kStageBytes + 2 * C::kStages * 8 + 16;
     int occ = 1;
     {
-        const cudaError_t e = kernel_setup((const void *)gemv_sk_kernel<BITS, MT, OCC>, smem, kSkThreads, smem, &occ);
+        const cudaError_t e = kernel_setup((const void *)gemv_sk_kernel<BITS, MT, OCC, EPI>, smem, kSkThreads, smem, &occ);
         if (e != cudaSuccess)
             return e;
     }
@@ -428,6 +442,7 @@ static cudaError_t launch_sk_t(const LinearArgs &a, void *ws, int sm_count, cuda
     p.y = a.y;
     p.KB = sh.kblocks();
     p.U = sh.panels() * sh.kblocks();
+    p.epi = a.epi ? *a.epi : EpiArgs{};
     p.cnt = (uint32_t *)ws;
     p.part = (float *)((uint8_t *)ws + ws_counter_bytes());
     int G = per_sm * sm_count;
@@ -445,18 +460,25 @@ static cudaError_t launch_sk_t(const LinearArgs &a, void *ws, int sm_count, cuda
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemv_sk_kernel<BITS, MT, OCC>, p);
+    return cudaLaunchKernelEx(&cfg, gemv_sk_kernel<BITS, MT, OCC, EPI>, p);
+}
+
+template <int BITS, int MT, bool EPI>
+static cudaError_t launch_sk_pick(const LinearArgs &a, int occ, void *ws, int sm_count, cudaStream_t st)
+{
+    switch (occ) {
+    case 1: return launch_sk_t<BITS, MT, 1, EPI>(a, ws, sm_count, st);
+    case 2: return launch_sk_t<BITS, MT, 2, EPI>(a, ws, sm_count, st);
+    case 4: return launch_sk_t<BITS, MT, 4, EPI>(a, ws, sm_count, st);
+    default: return launch_sk_t<BITS, MT, 3, EPI>(a, ws, sm_count, st);
+    }
 }
 
 template <int BITS, int MT>
 static cudaError_t launch_sk_occ(const LinearArgs &a, int occ, void *ws, int sm_count, cudaStream_t st)
 {
-    switch (occ) {
-    case 1: return launch_sk_t<BITS, MT, 1>(a, ws, sm_count, st);
-    case 2: return launch_sk_t<BITS, MT, 2>(a, ws, sm_count, st);
-    case 4: return launch_sk_t<BITS, MT, 4>(a, ws, sm_count, st);
-    default: return launch_sk_t<BITS, MT, 3>(a, ws, sm_count, st);
-    }
+    return a.epi ? launch_sk_pick<BITS, MT, true>(a, occ, ws, sm_count, st)
+                 : launch_sk_pick<BITS, MT, false>(a, occ, ws, sm_count, st);
 }
 
 cudaError_t launch_gemv_sk(const LinearArgs &a, int ctas_per_sm, void *ws, int sm_count, cudaStream_t st)
@@ -526,7 +548,7 @@ static cudaError_t launch_sk_noalloc_t(const LinearArgs &a, uint32_t *cnt, float
     constexpr size_t smem = 128 + (size_t)C::kStages * C::kStageBytes + 2 * C::kStages * 8 + 16;
     int occ = 1;
     {
-        const cudaError_t e = kernel_setup((const void *)gemv_sk_kernel<BITS, 1, OCC>, smem, kSkThreads, smem, &occ);
+        const cudaError_t e = kernel_setup((const void *)gemv_sk_kernel<BITS, 1, OCC, false>, smem, kSkThreads, smem, &occ);
         if (e != cudaSuccess)
             return e;
     }
@@ -543,6 +565,7 @@ static cudaError_t launch_sk_noalloc_t(const LinearArgs &a, uint32_t *cnt, float
     p.y = a.y;
     p.KB = sh.kblocks();
     p.U = sh.panels() * sh.kblocks();
+    p.epi = EpiArgs{};
     p.cnt = cnt;
     p.part = part;
     int G = per_sm * sm_count;
@@ -555,7 +578,7 @@ static cudaError_t launch_sk_noalloc_t(const LinearArgs &a, uint32_t *cnt, float
     cfg.blockDim = dim3(kSkThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, gemv_sk_kernel<BITS, 1, OCC>, p);
+    return cudaLaunchKernelEx(&cfg, gemv_sk_kernel<BITS, 1, OCC, false>, p);
 }
 
 int noalloc_max_m() { return kNoAllocMaxM; }

@@ -13,6 +13,17 @@ namespace wq {
 // inputs as consecutive chunks of kChunkTokens.
 constexpr int kChunkTokens = 128;
 constexpr int kMaxTokens = 65536;
+constexpr int kHeadChunk = 512; // tokens whose fp32 logits wq_linear_logprobs holds at once
+
+// The layer's epilogue (wq_epilogue.cuh): y = round(act(v + bias) * mul +
+// residual), absent parts NULL, in the activations' 16-bit format; or, with
+// out_f32, the accumulated value itself as fp32 (y then points to floats).
+struct EpiArgs {
+    const uint16_t *bias, *mul, *res;
+    long long ld_mul, ld_res; // row strides in elements
+    int act;                  // WQ_ACT_*
+    int out_f32;
+};
 
 struct LinearArgs {
     const uint16_t *x;
@@ -20,6 +31,7 @@ struct LinearArgs {
     const void *wq, *scales, *zeros;
     int bits, group;
     uint16_t *y;
+    const EpiArgs *epi = nullptr; // NULL: y = round(v)
 };
 
 // Split-K workspace: [counters, 256-byte padded][partials].
@@ -138,6 +150,13 @@ bool topk_plan(int M, int N, int k, int *S, int *P, int *T);
 size_t topk_ws_bytes(int M, int N, int k);
 cudaError_t launch_topk(const uint16_t *logits, int M, int N, int k, void *cand_ws, uint16_t *vals, int32_t *idx,
                         cudaStream_t st);
+
+// Log probabilities, entropy and the k best of M rows of N logits (dtype
+// WQ_DTYPE_*), ld elements apart; any output may be NULL, k = 0: no
+// alternatives.
+cudaError_t launch_logprobs(const void *logits, int dtype, int M, int N, long long ld, const int32_t *tokens, int k,
+                            float *logprob, float *entropy, float *top, int32_t *top_idx, int sm_count,
+                            cudaStream_t st);
 
 // Launch preparation of one kernel on the current device: raises its
 // dynamic shared-memory limit to smem_optin bytes (0: leave it) the first

@@ -1,0 +1,655 @@
+// wq_logprobs.cu -- log probabilities of given tokens, the entropy and the k
+// most likely alternatives of rows of logits, in one pass over the logits:
+//
+//     lse  = max_n x[n] + log sum_n exp(x[n] - max)
+//     logprob[t] = x[t] - lse
+//     entropy    = -sum_n p[n] log p[n] = log S - W / S,
+//                  S = sum_n exp(x[n] - max),  W = sum_n exp(x[n] - max) (x[n] - max)
+//     alternatives: the k largest x[n], ties to the lower index, as x[n] - lse
+//
+// Both terms of the entropy are positive (W <= 0, S >= 1), so it does not
+// cancel.  A thread keeps a running maximum with its S and W and rescales them
+// when the maximum grows, so every logit is read once and nothing is written
+// but the answers.
+//
+// Bound: HBM, 2 or 4 bytes per logit.  At that rate an SM has to take 12
+// 16-bit logits a clock, three quarters of what its exponential unit can do
+// and half of its issue slots, so the two sums run as packed fp32 pairs.
+//
+// Work split: a row goes to a cluster of C CTAs (1, 2, 4 or 8), each with one
+// contiguous slice of it, whose answers meet through distributed shared
+// memory: no workspace, no second launch, and one decode row still draws on
+// eight SMs.  A CTA reads its slice in batches of kUnroll 16-byte vectors per
+// thread, the next batch's loads in flight while it works on this one.
+//
+// Alternatives: a logit is a 64-bit key (value, then the complement of its
+// index), so all keys differ and the k largest are unique.  In the first batch
+// the largest key of every thread is known; a key that at least k of them
+// reach is found by a search over the keys with one block-wide count per
+// step, and only logits that reach it are kept (at most kUnroll vectors for
+// each thread counted, usually little more than k).  Later batches are only
+// compared with that bound, a vector at a time, and add the few that pass.
+// If a batch would overflow the list (rows that rise from end to end), the
+// list is cut back to its k best and the bound raised first.  At the end each
+// CTA sorts its best k by counting, and an entry's place in the row's answer
+// is its place in its own list plus the entries above it in the other CTAs'.
+#include <cfloat>
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "wq.h"
+#include "wq_device.cuh"
+#include "wq_internal.h"
+
+namespace wq {
+
+namespace {
+
+constexpr int kUnroll = 4;        // 16-byte vectors per thread and batch
+constexpr int kSortMax = 192;     // candidates ranked by counting without a cut first
+constexpr int kLpMaxCluster = 8;
+
+typedef unsigned long long key_t64;
+
+struct LpParams {
+    const void *logits;
+    long long ld;
+    int M, N, k, C, slice; // slice: elements per CTA, a multiple of the vector
+    const int32_t *tokens;
+    float *logprob, *entropy, *top;
+    int32_t *top_idx;
+};
+
+// The list must take what one bounded batch can add to k kept entries.
+__host__ __device__ constexpr int lp_accept(int k) { return k + k / 2 + 8; } // threads a bound may let through
+template <int VE>
+__host__ __device__ constexpr int lp_cap(int k)
+{
+    return lp_accept(k) * kUnroll * VE + k + 2 * VE; // + the elements outside the aligned vectors
+}
+
+template <class T>
+struct LpType;
+template <>
+struct LpType<__nv_bfloat16> {
+    static constexpr int VE = 8;
+    // largest of a vector, NaN if it holds one
+    static __device__ __forceinline__ float vmax(const uint4 &v)
+    {
+        uint32_t a, b;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a << 16)), "f"(__uint_as_float(a & 0xFFFF0000u)));
+        return r;
+    }
+    static __device__ __forceinline__ float2 pair(const uint4 &v, int i)
+    {
+        const uint32_t w = (&v.x)[i];
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+};
+template <>
+struct LpType<__half> {
+    static constexpr int VE = 8;
+    static __device__ __forceinline__ float vmax(const uint4 &v)
+    {
+        uint32_t a, b;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(f.x), "f"(f.y));
+        return r;
+    }
+    static __device__ __forceinline__ float2 pair(const uint4 &v, int i)
+    {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&(&v.x)[i]));
+    }
+};
+template <>
+struct LpType<float> {
+    static constexpr int VE = 4;
+    static __device__ __forceinline__ float vmax(const uint4 &v)
+    {
+        float a, b;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)));
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w)));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+        return a;
+    }
+    static __device__ __forceinline__ float2 pair(const uint4 &v, int i)
+    {
+        return make_float2(__uint_as_float((&v.x)[2 * i]), __uint_as_float((&v.x)[2 * i + 1]));
+    }
+};
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+
+// Bits that order like the value, -0 with +0 and every NaN above +inf.
+__device__ __forceinline__ uint32_t order32(float f)
+{
+    uint32_t b = __float_as_uint(f);
+    if (f != f)
+        return 0xFFFFFFFFu;
+    if (f == 0.f)
+        b = 0;
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float value32(uint32_t o)
+{
+    if (o == 0xFFFFFFFFu)
+        return __uint_as_float(0x7FFFFFFFu);
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+
+// Every key is above 0, which stands for "none" (order32 > 0: the smallest, of
+// -inf, is 0x007FFFFF).
+__device__ __forceinline__ key_t64 make_key(float f, int idx)
+{
+    return ((key_t64)order32(f) << 32) | (uint32_t)~idx;
+}
+
+// ---------------------------------------------------------------------------
+// Running softmax sums
+// ---------------------------------------------------------------------------
+constexpr float kFarBelow = -200.f; // exp(-200) is 0 in fp32: masked and far logits add nothing, and 0 * -inf never forms
+
+__device__ __forceinline__ float diff_clamped(float x, float m) // NaN stays NaN
+{
+    float d = x - m;
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(kFarBelow));
+    return d;
+}
+
+__device__ __forceinline__ float exp_nat(float d)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * 1.4426950408889634f));
+    return e;
+}
+
+struct Sums {
+    float m, s, w; // maximum, sum of exp(x - m), sum of exp(x - m) (x - m)
+};
+
+__device__ __forceinline__ void rescale(Sums &a, float m)
+{
+    const float d = fmaxf(a.m - m, kFarBelow), c = exp_nat(d);
+    a.w = c * fmaf(a.s, d, a.w);
+    a.s *= c;
+    a.m = m;
+}
+
+__device__ __forceinline__ void merge(Sums &a, Sums b)
+{
+    const float m = fmaxf(a.m, b.m);
+    rescale(a, m);
+    rescale(b, m);
+    a.s += b.s;
+    a.w += b.w;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b),
+                          z = *reinterpret_cast<unsigned long long *>(&c);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
+// ---------------------------------------------------------------------------
+// Cluster (distributed shared memory)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float cluster_ld_f32(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ key_t64 cluster_ld_u64(uint32_t a)
+{
+    key_t64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// Selection
+// ---------------------------------------------------------------------------
+
+// A bound that between k and lp_accept(k) of the threads' keys reach, or 0
+// if fewer than k threads have one.  The keys differ, so the search ends: its
+// interval halves, and a bound with exactly k above it exists.  Called by the
+// whole CTA.
+__device__ __forceinline__ key_t64 bound_of_threads(key_t64 mine, int k)
+{
+    key_t64 lo = 0, hi = ~0ull; // at least k reach lo (0: everything); fewer than k reach hi
+    if (__syncthreads_count(mine != 0) < k)
+        return 0;
+    for (;;) {
+        const key_t64 mid = lo + (hi - lo) / 2;
+        if (mid == lo)
+            return lo;
+        const int c = __syncthreads_count(mine >= mid);
+        if (c >= k && c <= lp_accept(k))
+            return mid;
+        if (c < k)
+            hi = mid;
+        else
+            lo = mid;
+    }
+}
+
+// The same over the n keys of a list, each thread counting its share.
+__device__ __forceinline__ key_t64 bound_of_list(const key_t64 *list, int n, int k, int *s_count)
+{
+    key_t64 lo = 0, hi = ~0ull;
+    for (int slot = 0;; slot ^= 1) {
+        const key_t64 mid = lo + (hi - lo) / 2;
+        if (mid == lo)
+            return lo;
+        if (threadIdx.x == 0)
+            s_count[slot] = 0;
+        __syncthreads();
+        int c = 0;
+        for (int i = threadIdx.x; i < n; i += blockDim.x)
+            c += list[i] >= mid;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if ((threadIdx.x & 31) == 0 && c)
+            atomicAdd(&s_count[slot], c);
+        __syncthreads();
+        c = s_count[slot];
+        if (c >= k && c <= lp_accept(k))
+            return mid;
+        if (c < k)
+            hi = mid;
+        else
+            lo = mid;
+    }
+}
+
+// Ranks the n keys of src (n <= kSortMax, all different) by counting, the k
+// largest in order into dst, 0 behind them if there are fewer.
+__device__ __forceinline__ void rank_into(const key_t64 *src, int n, int k, key_t64 *dst)
+{
+    for (int i = threadIdx.x; i < k; i += blockDim.x)
+        if (i >= n)
+            dst[i] = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const key_t64 mine = src[i];
+        int above = 0;
+        for (int j = 0; j < n; ++j)
+            above += src[j] > mine;
+        if (above < k)
+            dst[above] = mine;
+    }
+    __syncthreads();
+}
+
+struct LpShared {
+    key_t64 cut[kSortMax];      // a list cut back before it is ranked
+    key_t64 best[kTopkMaxK];    // this CTA's k best, in order
+    key_t64 others[kLpMaxCluster * kTopkMaxK];
+    Sums warp_sums[32];
+    Sums sums; // this CTA's
+    int count; // entries of the list
+    int cut_count;
+    int list_count[2];
+};
+
+// The list's k best, in order, into sh.best.
+__device__ __forceinline__ void sort_list(LpShared &sh, const key_t64 *list, int n, int k)
+{
+    if (n <= kSortMax) {
+        rank_into(list, n, k, sh.best);
+        return;
+    }
+    const key_t64 b = bound_of_list(list, n, k, sh.list_count);
+    if (threadIdx.x == 0)
+        sh.cut_count = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (list[i] >= b)
+            sh.cut[atomicAdd(&sh.cut_count, 1)] = list[i]; // at most lp_accept(k) <= kSortMax
+    __syncthreads();
+    rank_into(sh.cut, sh.cut_count, k, sh.best);
+}
+static_assert(lp_accept(kTopkMaxK) <= kSortMax, "a cut list can be ranked");
+
+template <class T, int THREADS, bool TOPK>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const LpParams p)
+{
+    using L = LpType<T>;
+    constexpr int VE = L::VE, B = THREADS * kUnroll; // vectors per batch
+    extern __shared__ key_t64 s_list[];              // lp_cap(k) candidates (TOPK)
+    __shared__ LpShared sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = p.C > 1 ? (int)cluster_rank() : 0;
+    const int m = blockIdx.x / p.C, k = p.k;
+    const int cap = lp_cap<VE>(k);
+
+    pdl_launch_dependents();
+    pdl_wait(); // the logits may come from the preceding kernel
+
+    const T *row = static_cast<const T *>(p.logits) + (long long)m * p.ld;
+    const int e0 = min(p.N, rank * p.slice), e1 = min(p.N, e0 + p.slice);
+    // whole aligned vectors [v0, v0 + nv VE); the elements before and after them one by one
+    const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(row + e0) & 15)) & 15) / (int)sizeof(T);
+    const int v0 = min(e1, e0 + lead), nv = (e1 - v0) / VE;
+    const uint4 *vec = reinterpret_cast<const uint4 *>(row + v0);
+
+    int token = -1;
+    float x_token = 0.f;
+    if (rank == 0 && threadIdx.x == 0 && p.tokens) {
+        token = p.tokens[m];
+        if (token >= 0 && token < p.N)
+            x_token = to_float(row[token]);
+    }
+
+    constexpr uint32_t minus_inf = std::is_same_v<T, float> ? 0xFF800000u
+                                   : std::is_same_v<T, __half> ? 0xFC00FC00u
+                                                               : 0xFF80FF80u;
+    const uint4 none = make_uint4(minus_inf, minus_inf, minus_inf, minus_inf);
+    uint4 cur[kUnroll], nxt[kUnroll];
+    auto load = [&](int b, uint4(&v)[kUnroll]) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = b + u * THREADS + (int)threadIdx.x;
+            v[u] = i < nv ? ldg_stream(vec + i) : none;
+        }
+    };
+    load(0, cur);
+
+    Sums a{-FLT_MAX, 0.f, 0.f};
+    key_t64 bound = 0;
+    float bound_f = -INFINITY; // the bound's value, once a batch has set it
+
+    // the up to 2 VE elements outside the aligned vectors: one thread each
+    const int tail0 = v0 + nv * VE;
+    const int edge = (int)threadIdx.x < v0 - e0            ? e0 + (int)threadIdx.x
+                     : (int)threadIdx.x < v0 - e0 + e1 - tail0 ? tail0 + (int)threadIdx.x - (v0 - e0)
+                                                               : -1;
+    float edge_x = 0.f;
+    if (edge >= 0) {
+        edge_x = to_float(row[edge]);
+        a.m = fmaxf(a.m, edge_x);
+        const float d = diff_clamped(edge_x, a.m);
+        a.s = exp_nat(d);
+        a.w = a.s * d;
+    }
+    if constexpr (TOPK) {
+        if (threadIdx.x == 0)
+            sh.count = 0;
+        __syncthreads();
+        if (edge >= 0)
+            s_list[atomicAdd(&sh.count, 1)] = make_key(edge_x, edge);
+    }
+
+    for (int b = 0; b == 0 || b < nv; b += B) {
+        const bool more = b + B < nv;
+        if (more)
+            load(b + B, nxt);
+        // ---- running softmax sums ----
+        float vm[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            vm[u] = L::vmax(cur[u]);
+        float bm = vm[0];
+#pragma unroll
+        for (int u = 1; u < kUnroll; ++u)
+            bm = fmaxf(bm, vm[u]);
+        if (bm > a.m)
+            rescale(a, bm);
+        float2 s2 = make_float2(0.f, 0.f), w2 = s2;
+        const float2 nm = make_float2(-a.m, -a.m);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int i = 0; i < VE / 2; ++i) {
+                float2 d = add2(L::pair(cur[u], i), nm);
+                asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.x) : "f"(kFarBelow));
+                asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.y) : "f"(kFarBelow));
+                const float2 e = make_float2(exp_nat(d.x), exp_nat(d.y));
+                s2 = add2(s2, e);
+                w2 = fma2(e, d, w2);
+            }
+        a.s += s2.x + s2.y;
+        a.w += w2.x + w2.y;
+
+        // ---- candidates ----
+        if constexpr (TOPK) {
+            // the largest key of this thread's batch (bound 0: of everything there is)
+            auto largest = [&]() {
+                key_t64 best = 0;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int i = b + u * THREADS + (int)threadIdx.x;
+                    if (i < nv)
+#pragma unroll
+                        for (int j = 0; j < VE / 2; ++j) {
+                            const float2 f = L::pair(cur[u], j);
+                            const key_t64 k0 = make_key(f.x, v0 + i * VE + 2 * j), k1 = make_key(f.y, v0 + i * VE + 2 * j + 1);
+                            best = best > k0 ? best : k0;
+                            best = best > k1 ? best : k1;
+                        }
+                }
+                return best;
+            };
+            // appends the keys that reach the bound; an overfull list only counts on
+            auto append = [&]() {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int i = b + u * THREADS + (int)threadIdx.x;
+                    if (i < nv && !(vm[u] < bound_f))
+#pragma unroll
+                        for (int j = 0; j < VE / 2; ++j) {
+                            const float2 f = L::pair(cur[u], j);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const key_t64 key = make_key(h ? f.y : f.x, v0 + i * VE + 2 * j + h);
+                                if (key >= bound) {
+                                    const int at = atomicAdd(&sh.count, 1);
+                                    if (at < cap)
+                                        s_list[at] = key;
+                                }
+                            }
+                        }
+                }
+            };
+            if (b == 0) {
+                bound = bound_of_threads(largest(), k);
+                bound_f = bound ? value32((uint32_t)(bound >> 32)) : -INFINITY;
+                append();
+            } else {
+                bool any = false;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+                    any |= !(vm[u] < bound_f);
+                // the list's length before this batch, to go back to if it overflows
+                const bool some = __syncthreads_or(any);
+                if (some) {
+                    const int before = sh.count;
+                    __syncthreads();
+                    append();
+                    __syncthreads();
+                    if (sh.count > cap) { // keep the k best so far, raise the bound, take the batch again
+                        sort_list(sh, s_list, before, k);
+                        const key_t64 kth = sh.best[k - 1];
+                        bound = bound_of_threads(largest(), k);
+                        bound = bound > kth ? bound : kth;
+                        bound_f = bound ? value32((uint32_t)(bound >> 32)) : -INFINITY;
+                        const int keep = min(before, k);
+                        for (int i = threadIdx.x; i < keep; i += THREADS)
+                            s_list[i] = sh.best[i];
+                        if (threadIdx.x == 0)
+                            sh.count = keep;
+                        __syncthreads();
+                        append();
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            cur[u] = nxt[u];
+    }
+
+    // ---- the CTA's sums: lanes, then warps, in a fixed order ----
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Sums x;
+        x.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+        x.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+        x.w = __shfl_xor_sync(0xffffffffu, a.w, o);
+        // the lower lane's half first on both sides, so that both form the same sum
+        Sums lo = (lane & o) ? x : a, hi = (lane & o) ? a : x;
+        merge(lo, hi);
+        a = lo;
+    }
+    if (lane == 0)
+        sh.warp_sums[warp] = a;
+    __syncthreads(); // also: every candidate is in the list
+    Sums t = sh.warp_sums[0];
+    for (int i = 1; i < THREADS / 32; ++i)
+        merge(t, sh.warp_sums[i]);
+    if constexpr (TOPK)
+        sort_list(sh, s_list, sh.count, k);
+    if (p.C > 1) {
+        if (threadIdx.x == 0)
+            sh.sums = t;
+        cluster_sync();
+        t = Sums{-FLT_MAX, 0.f, 0.f};
+        for (int c = 0; c < p.C; ++c) {
+            const uint32_t at = cluster_addr(&sh.sums, c);
+            Sums x;
+            x.m = cluster_ld_f32(at);
+            x.s = cluster_ld_f32(at + 4);
+            x.w = cluster_ld_f32(at + 8);
+            merge(t, x);
+        }
+        if constexpr (TOPK)
+            for (int i = threadIdx.x; i < p.C * k; i += THREADS)
+                sh.others[i] = cluster_ld_u64(cluster_addr(&sh.best[i % k], i / k));
+        cluster_sync(); // no CTA leaves while another reads its shared memory
+    }
+    const float log_s = logf(t.s);
+    if (rank == 0 && threadIdx.x == 0) {
+        if (p.logprob)
+            p.logprob[m] = token >= 0 && token < p.N ? (x_token - t.m) - log_s : __uint_as_float(0x7FFFFFFFu);
+        if (p.entropy)
+            p.entropy[m] = log_s - t.w / t.s;
+    }
+    if constexpr (TOPK) {
+        for (int i = threadIdx.x; i < k; i += THREADS) {
+            const key_t64 key = sh.best[i];
+            if (key == 0)
+                continue; // this slice is shorter than k
+            int at = i;
+            for (int c = 0; c < p.C && p.C > 1; ++c) {
+                if (c == rank)
+                    continue;
+                const key_t64 *o = sh.others + c * k;
+                int lo = 0, hi = k; // entries of a descending list above key
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (o[mid] > key)
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
+                at += lo;
+            }
+            if (at < k) {
+                p.top[(size_t)m * k + at] = (value32((uint32_t)(key >> 32)) - t.m) - log_s;
+                p.top_idx[(size_t)m * k + at] = (int32_t)~(uint32_t)key;
+            }
+        }
+    }
+}
+
+template <class T, int THREADS, bool TOPK>
+cudaError_t launch_lp(LpParams p, int sm_count, cudaStream_t st)
+{
+    constexpr int VE = LpType<T>::VE;
+    const size_t smem = TOPK ? (size_t)lp_cap<VE>(p.k) * sizeof(key_t64) : 0;
+    const void *f = (const void *)logprobs_kernel<T, THREADS, TOPK>;
+    cudaError_t e = kernel_setup(f, smem, 0, 0, nullptr);
+    if (e != cudaSuccess)
+        return e;
+    // CTAs of a row: while they fit the GPU at once with the others', and each
+    // has a batch's work at least
+    const long long slots = (long long)sm_count * (1024 / THREADS);
+    int C = 1;
+    while (C < kLpMaxCluster && (long long)p.M * C * 2 <= slots && p.N / (2 * C) >= THREADS * VE)
+        C *= 2;
+    p.C = C;
+    p.slice = ((p.N + C - 1) / C + VE - 1) / VE * VE;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    cfg.gridDim = dim3((unsigned)p.M * C);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS, TOPK>, p);
+}
+
+template <class T>
+cudaError_t launch_lp_type(const LpParams &p, int sm_count, cudaStream_t st)
+{
+    return p.k > 0 ? launch_lp<T, 512, true>(p, sm_count, st) : launch_lp<T, 512, false>(p, sm_count, st);
+}
+
+} // namespace
+
+cudaError_t launch_logprobs(const void *logits, int dtype, int M, int N, long long ld, const int32_t *tokens, int k,
+                            float *logprob, float *entropy, float *top, int32_t *top_idx, int sm_count,
+                            cudaStream_t st)
+{
+    LpParams p{logits, ld, M, N, k, 1, N, tokens, logprob, entropy, top, top_idx};
+    switch (dtype) {
+    case WQ_DTYPE_BF16: return launch_lp_type<__nv_bfloat16>(p, sm_count, st);
+    case WQ_DTYPE_F16: return launch_lp_type<__half>(p, sm_count, st);
+    default: return launch_lp_type<float>(p, sm_count, st);
+    }
+}
+
+} // namespace wq
