@@ -200,6 +200,19 @@ int lookup_choice(const DeviceInfo &d, int M, int K, int N, int bits, int group,
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA; }
 
+// The workspace registered for the current device, if any.
+void registered_workspace(void **w, size_t *have)
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto it = g_ws.find(dev);
+    if (it != g_ws.end()) {
+        *w = it->second.first;
+        *have = it->second.second;
+    }
+}
+
 // One call of at most kChunkTokens tokens: the dispatcher's (or the forced)
 // kernel for this M, with its epilogue (NULL: none).
 int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros, int group,
@@ -228,16 +241,8 @@ int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *sc
     // the workspace this call would use (explicit, else the registered one)
     void *w = ws;
     size_t have = ws_bytes_given;
-    if (!w) {
-        int dev = 0;
-        cudaGetDevice(&dev);
-        std::lock_guard<std::mutex> lk(g_mu);
-        auto it = g_ws.find(dev);
-        if (it != g_ws.end()) {
-            w = it->second.first;
-            have = it->second.second;
-        }
-    }
+    if (!w)
+        registered_workspace(&w, &have);
     if (w && !aligned16(w))
         return WQ_ERR_ALIGN;
     const bool sk_ws_ok = w && have >= ws_bytes_gemv_sk(M, N);
@@ -312,6 +317,10 @@ int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *sc
     return cuda_status(launch_gemm(a, c.split, c.split > 1 ? w : nullptr, d.sm_count, stream));
 }
 
+int linear_prompt(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros, int bits,
+                  int group, int N, uint16_t *y, void *ws, size_t ws_bytes_given, cudaStream_t stream,
+                  const EpiArgs &epi);
+
 // The epilogue of the token rows from m0 on.
 EpiArgs epi_rows_from(const EpiArgs &e, int m0)
 {
@@ -337,6 +346,8 @@ int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *sca
     if (bits_of_group(group, &bits) != WQ_OK)
         return WQ_ERR_GROUP;
     const int chunk = chunk_tokens(bits, lgroup_of(bits, K, group));
+    if (epi && M > kChunkTokens && chunk == kChunkTokens && variant == WQ_VARIANT_AUTO)
+        return linear_prompt(x, M, K, Wq, scales, zeros, bits, group, N, y, ws, ws_bytes_given, stream, *epi);
     if (M <= chunk)
         return linear_chunk(x, M, K, Wq, scales, zeros, group, N, y, variant, split, ws, ws_bytes_given, stream, epi);
     if (M > kMaxTokens)
@@ -352,6 +363,45 @@ int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *sca
         const int st = linear_chunk(x + (size_t)m0 * K, mc, K, Wq, scales, zeros, group, N, y + y_off, variant, split,
                                     ws, ws_bytes_given, stream, epi ? &ec : nullptr);
         if (st != WQ_OK)
+            return st;
+    }
+    return WQ_OK;
+}
+
+// A prompt (M > kChunkTokens) with an epilogue: the prompt GEMM, in one launch
+// unless its unit count would leave 32 bits.
+int linear_prompt(const uint16_t *x, int M, int K, const void *Wq, const void *scales, const void *zeros, int bits,
+                  int group, int N, uint16_t *y, void *ws, size_t ws_bytes_given, cudaStream_t stream,
+                  const EpiArgs &epi)
+{
+    if (!x || !Wq || !scales || !y || (bits == 4 && !zeros))
+        return WQ_ERR_NULL;
+    int st = check_weight_shape(bits, K, N, group);
+    if (st != WQ_OK)
+        return st;
+    if (M > kMaxTokens)
+        return WQ_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(Wq) || !aligned16(scales) || (zeros && !aligned16(zeros)))
+        return WQ_ERR_ALIGN;
+    DeviceInfo d;
+    if ((st = current_device_info(&d)) != WQ_OK)
+        return st;
+    if (d.major != 10)
+        return WQ_ERR_ARCH;
+    void *w = ws;
+    size_t have = ws_bytes_given;
+    if (!w)
+        registered_workspace(&w, &have);
+    if (w && !aligned16(w))
+        return WQ_ERR_ALIGN;
+    if (w && have < ws_bytes_gemm_pf())
+        w = nullptr; // whole tiles only
+    const int most = pf_max_tokens(K, N);
+    for (int m0 = 0; m0 < M; m0 += most) {
+        const EpiArgs ec = epi_rows_from(epi, m0);
+        LinearArgs a{x + (size_t)m0 * K, std::min(most, M - m0), K, N, Wq, scales, zeros, bits, bits == 8 ? 0 : 128,
+                     y + (size_t)m0 * N * (epi.out_f32 ? 2 : 1), &ec};
+        if ((st = cuda_status(launch_gemm_pf(a, w, d.sm_count, stream))) != WQ_OK)
             return st;
     }
     return WQ_OK;
@@ -1082,12 +1132,13 @@ int wq_wait_selftest(int limit_us, cudaStream_t stream)
 
 int wq_device_error(cudaStream_t stream)
 {
-    int a = 0, b = 0, c = 0, e = 0, f = 0, h = 0;
+    int a = 0, b = 0, c = 0, e = 0, f = 0, h = 0, pf = 0;
     if (read_device_error(&a, stream) != cudaSuccess || read_gemv_sk_error(&b, stream) != cudaSuccess ||
         read_gemm_sk_error(&c, stream) != cudaSuccess || read_gemm_i8_error(&e, stream) != cudaSuccess ||
-        read_gemm_i4_error(&f, stream) != cudaSuccess || read_gemm_w4_error(&h, stream) != cudaSuccess)
+        read_gemm_i4_error(&f, stream) != cudaSuccess || read_gemm_w4_error(&h, stream) != cudaSuccess ||
+        read_gemm_pf_error(&pf, stream) != cudaSuccess)
         return WQ_ERR_CUDA;
-    return (a == 0 && b == 0 && c == 0 && e == 0 && f == 0 && h == 0) ? WQ_OK : WQ_ERR_TIMEOUT;
+    return (a == 0 && b == 0 && c == 0 && e == 0 && f == 0 && h == 0 && pf == 0) ? WQ_OK : WQ_ERR_TIMEOUT;
 }
 
 } // extern "C"

@@ -1,0 +1,766 @@
+// wq_gemm_pf.cu -- the layer over a prompt: W8A16 and W4A16 (group 128) for
+// many tokens, on pairs of SMs.
+//
+//     v[m][n] = s[n] sum_k q[n][k] x[m][k]                        (INT8)
+//     v[m][n] = sum_g s[n][g] sum_{k in g} (q[n][k] - z[n][g]) x[m][k]   (INT4)
+//
+// then the epilogue (wq_epilogue.cuh).  The tensor cores take the exact
+// integers q and q - z in the activations' format; the only rounding before
+// the epilogue is the fp32 accumulation.
+//
+// Bound: the tensor cores.  Two CTAs (a cluster, one on each SM of a pair)
+// work on one tile of 256 output channels x up to 192 tokens with
+// tcgen05.mma.cta_group::2: each CTA holds its own 128 channels' weights and
+// accumulators in its tensor memory and half of the tokens' activations in
+// its shared memory, so an activation byte is brought in once for 256
+// channels.  A CTA alone (128 x 192) would have to fill 48 KB of activations
+// per 128 k, more than L2 gives an SM in the time of its products.
+//
+// A step is 64 k of a tile: four MMAs of K = 16.  Tensor memory: two
+// accumulators of 192 columns (INT4: a group's sums, retired into fp32
+// register totals while the next group is multiplied; INT8: a whole tile's
+// sums, written out while the next tile is multiplied) and four A stages of 32
+// columns.  The token tile is M cut into equal parts of at most 192, rounded
+// up to 16, so ragged prompts waste little.
+//
+// Work: units (tile, 128-k block), tiles of one channel panel pair next to each
+// other; each pair of CTAs takes an equal contiguous run of units (stream-K,
+// the partial sums of a tile that two or more pairs share are added in their
+// order by the last to arrive), or whole tiles where there is no workspace.
+//
+// Warps (640 threads; registers are moved to the retire warps):
+//   0      x producer: the CTA's half of the token tile, 64 k a step (tensor
+//          map, 128-byte swizzle), signalled on the leader's barrier
+//   1      weight producer: a unit's packed block (and zero points, scales)
+//   2      tensor memory; in the leader CTA, the thread that issues the MMAs
+//   4-11   retire warps: lane quadrant x half of the token columns
+//   12-19  dequantization: packed block -> exact integers in tensor memory
+// One commit per step, to both CTAs, tells the x producers (8 stages), the
+// dequantization (4) and, for INT4, the retire warps (2 groups) that the step
+// is done.  Every wait is bounded (2 s); a timeout is recorded and every role
+// winds down.
+#include <cstdint>
+
+#include "wq.h"
+#include "wq_device.cuh"
+#include "wq_epilogue.cuh"
+#include "wq_gemm_common.cuh"
+#include "wq_internal.h"
+
+namespace wq {
+
+static __device__ int g_gemm_pf_error = 0;
+
+namespace {
+
+constexpr int kPfThreads = 640;
+constexpr int kPfRegsIssue = 32, kPfRegsRetire = 168, kPfRegsDequant = 56; // registers a thread, by role
+constexpr int kPfTok = 192;   // columns of an accumulator
+constexpr int kPfA0 = 2 * kPfTok; // first A column
+constexpr int kPfAS = 4;      // A stages (64 k, 32 columns)
+constexpr int kPfXS = 8;      // x stages (64 k); also the steps' barriers: operands complete, products done
+constexpr int kPfSS = 16;     // scale stages
+constexpr int kPfXB = kPfTok / 2 * 128; // bytes of an x stage
+constexpr int kPfChunks = kPfTok / 32;  // 16-column chunks of a retire warp, at most
+static_assert(kPfA0 + kPfAS * 32 == 512, "tensor memory plan");
+static_assert(kPfXS == 8 && kPfXS >= kPfAS, "a step's barriers are read before their slot comes round (two groups are four steps)");
+
+template <int BITS>
+struct PfCfg {
+    static constexpr int kWB = BITS == 4 ? 8192 : 16384;
+    static constexpr int kWS = BITS == 4 ? 8 : 6;
+};
+
+struct PfParams {
+    int M, N, KB, U, TT, n, tiles, panels; // n: tokens of a tile (a multiple of 16)
+    int align;                             // 1: whole tiles per pair
+    const uint8_t *wq;
+    const uint16_t *scales;
+    const uint8_t *zeros;
+    uint16_t *y;
+    EpiArgs epi;
+    float *part;   // [pairs][2 slots][2 CTAs][kPfTok tokens][128 rows]
+    uint32_t *cnt; // [pairs][2 CTAs][8 warps], by a split tile's first pair
+};
+
+template <int BITS>
+constexpr size_t pf_smem_bytes()
+{
+    using C = PfCfg<BITS>;
+    return 1024 + (size_t)kPfXS * kPfXB + (size_t)C::kWS * C::kWB + (size_t)kPfSS * 256 + (size_t)C::kWS * 128 +
+           (size_t)(2 * kPfXS + 2 * C::kWS + 2 * kPfSS + 4) * 8 + 16;
+}
+
+// ---- pairs of CTAs ----
+__device__ __forceinline__ uint32_t pf_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t pf_map(const void *p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+// Arrival on a barrier of either CTA.  What it hands over is in tensor memory,
+// ordered by tcgen05.fence; a release at cluster scope, which it does not need,
+// took 1400 cycles.
+__device__ __forceinline__ void pf_arrive(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ bool pf_elect() // one lane of the (converged) warp
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+__device__ __forceinline__ void pf_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pf_tmem_alloc(uint32_t *dst)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pf_tmem_dealloc(uint32_t taddr)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+}
+// x box into this CTA's shared memory, completing on the leader's barrier.
+__device__ __forceinline__ void pf_load_x(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t cluster_bar,
+                                          uint64_t policy)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(c0), "r"(c1), "r"(cluster_bar), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void pf_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// Arrives on the barrier at this address in both CTAs when the MMAs issued so
+// far have completed.
+__device__ __forceinline__ void pf_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+__device__ __forceinline__ void pf_ffma2(float &d0, float &d1, float a, float b0, float b1)
+{
+    unsigned long long d, aa, bb;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(d0), "f"(d1));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(bb) : "f"(b0), "f"(b1));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(aa), "l"(bb));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+}
+
+// Two int8 codes (bytes lo, lo + 1 of w) as exact bf16: with the low seven
+// bits, 0x4300 | c is 128 + c; with the sign bit, 0x4300 | 0x80 is 256.
+__device__ __forceinline__ uint32_t pf_s8pair(uint32_t w, int h)
+{
+    const uint32_t b = __byte_perm(w, 0u, h == 0 ? 0x4140u : 0x4342u);
+    uint32_t mag, off;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(mag) : "r"(b), "r"(0x007F007Fu), "r"(0x43004300u));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(off) : "r"(b), "r"(0x00800080u), "r"(0x43004300u));
+    return bf16x2_sub(mag, off);
+}
+
+template <int BITS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
+    gemm_pf_kernel(const __grid_constant__ CUtensorMap tmx, const PfParams p)
+{
+    using C = PfCfg<BITS>;
+    constexpr int WS = C::kWS, WB = C::kWB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sX = smem;                // kPfXS x stages, 1024-byte aligned
+    uint8_t *sW = sX + kPfXS * kPfXB;  // WS packed blocks
+    uint8_t *sS = sW + (size_t)WS * WB; // kPfSS group scales
+    uint8_t *sZ = sS + kPfSS * 256;    // WS zero points
+    uint64_t *full = reinterpret_cast<uint64_t *>(sZ + WS * 128);
+    uint64_t *done = full + kPfXS;
+    uint64_t *wfull = done + kPfXS, *wempty = wfull + WS;
+    uint64_t *sfull = wempty + WS, *sempty = sfull + kPfSS;
+    uint64_t *accfull = sempty + kPfSS, *accempty = accfull + 2;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(accempty + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = pf_rank();
+    const int G = gridDim.x >> 1, pair = blockIdx.x >> 1, KB = p.KB;
+    // this pair's units [u0, u1)
+    auto start_of = [&](int c) {
+        return p.align ? sk_start(p.tiles, G, c) * KB : sk_start(p.U, G, c);
+    };
+    const int u0 = start_of(pair), u1 = start_of(pair + 1), nu = u1 - u0;
+    const int tile0 = u0 / KB, kb0 = u0 % KB;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPfXS; ++s) {
+            mbar_init(&full[s], 17); // the dequantization warps of both CTAs and the leader's expect_tx
+            mbar_init(&done[s], 1);
+        }
+        for (int s = 0; s < WS; ++s) {
+            mbar_init(&wfull[s], 1);
+            mbar_init(&wempty[s], 8);
+        }
+        for (int s = 0; s < kPfSS; ++s) {
+            mbar_init(&sfull[s], 1);
+            mbar_init(&sempty[s], 8);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&accfull[s], 1);
+            mbar_init(&accempty[s], 16); // the retire warps of both CTAs
+        }
+        fence_mbar_init();
+    }
+    if (warp == 2)
+        pf_tmem_alloc(s_tmem);
+    if (warp == 0 && lane == 0)
+        prefetch_tensormap(&tmx);
+    tc_fence_before();
+    __syncthreads();
+    pf_cluster_sync(); // both CTAs' barriers exist
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = *s_tmem;
+    bool ok = true;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfRegsIssue));
+        if (warp == 0 && lane == 0) {
+            // ---------------- x producer ----------------
+            pdl_wait(); // x may be written by the preceding kernel
+            const uint64_t pol = policy_evict_last();
+            const int half = p.n >> 1, tx = p.n * 128; // both CTAs' bytes
+            const uint32_t bar = pf_map(full, 0);
+            int kb = kb0, tt = tile0 % p.TT, c1 = tt * p.n + (int)rank * half;
+            for (int i = 0; i < 2 * nu; ++i) {
+                const int xs = i % kPfXS;
+                if (i >= kPfXS && !mbar_wait(&done[xs], ((i / kPfXS) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (rank == 0)
+                    mbar_arrive_expect_tx(&full[xs], tx);
+                pf_load_x(sX + xs * kPfXB, &tmx, kb * kBlockK + (i & 1) * 64, c1, bar + xs * 8, pol);
+                if ((i & 1) && ++kb == KB) {
+                    kb = 0;
+                    if (++tt == p.TT)
+                        tt = 0;
+                    c1 = tt * p.n + (int)rank * half;
+                }
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ---------------- weight producer ----------------
+            const uint64_t pol = policy_evict_first();
+            int kb = kb0, tt = tile0 % p.TT, pnl = 2 * (tile0 / p.TT) + (int)rank;
+            int ws = 0;
+            uint32_t wpar = 1; // the stage's last round; its first needs no wait
+            for (int i = 0; i < nu; ++i) {
+                if (i >= WS && !mbar_wait(&wempty[ws], wpar)) {
+                    ok = false;
+                    break;
+                }
+                const size_t blk = (size_t)pnl * KB + kb;
+                if (pnl < p.panels) {
+                    mbar_arrive_expect_tx(&wfull[ws], WB + (BITS == 4 ? 64 : 0));
+                    bulk_g2s(sW + (size_t)ws * WB, p.wq + blk * WB, WB, &wfull[ws], pol);
+                    if constexpr (BITS == 4)
+                        bulk_g2s(sZ + ws * 128, p.zeros + blk * 64, 64, &wfull[ws], pol);
+                } else {
+                    mbar_arrive(&wfull[ws]); // no such panel: its rows are never written
+                }
+                if constexpr (BITS == 4) {
+                    const int ss = i % kPfSS;
+                    if (i >= kPfSS && !mbar_wait(&sempty[ss], ((i / kPfSS) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (pnl < p.panels) {
+                        mbar_arrive_expect_tx(&sfull[ss], 256);
+                        bulk_g2s(sS + ss * 256, p.scales + blk * kPanelRows, 256, &sfull[ss], pol);
+                    } else {
+                        mbar_arrive(&sfull[ss]);
+                    }
+                }
+                if (++ws == WS) {
+                    ws = 0;
+                    wpar ^= 1;
+                }
+                if (++kb == KB) {
+                    kb = 0;
+                    if (++tt == p.TT) {
+                        tt = 0;
+                        pnl += 2;
+                    }
+                }
+            }
+        } else if (warp == 2 && rank == 0) {
+            // ---------------- MMA issuer ----------------
+            // The whole warp walks the steps, so that addresses and descriptors
+            // stay in uniform registers; one lane issues.  Unrolled over the ring,
+            // whose slots, stages and parities are then constants: the loop's own
+            // instructions cost as much as the products otherwise.
+            const bool issuer = pf_elect();
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.n >> 3) << 17) | (16u << 24);
+            const uint64_t bdesc0 = smem_desc_sw128(smem_u32(sX));
+            const int steps = 2 * nu;
+            int kb = kb0, acc = 0; // acc: tiles begun (INT8)
+            uint32_t par = 0;
+            for (int i0 = 0; i0 < steps && ok; i0 += kPfXS, par ^= 1) {
+#pragma unroll
+                for (int j = 0; j < kPfXS; ++j) {
+                    if (i0 + j >= steps)
+                        break;
+                    bool fresh = (j & 1) == 0;
+                    int b = (j >> 1) & 1;
+                    if constexpr (BITS == 8) {
+                        fresh = fresh && (kb == 0 || i0 + j == 0);
+                        acc += fresh;
+                        b = (acc - 1) & 1;
+                    }
+                    if (fresh) { // the accumulator's last use must have been read
+                        bool free = true;
+                        if constexpr (BITS == 4) // group g = (i0 + j) / 2 waits for the release of g - 2
+                            free = (i0 == 0 && j < 4) || mbar_wait(&accempty[b], ((j >> 2) + 1) & 1);
+                        else
+                            free = acc <= 2 || mbar_wait(&accempty[b], ((acc - 3) >> 1) & 1);
+                        ok = ok && free;
+                    }
+                    ok = ok && mbar_wait(&full[j], par);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (issuer) {
+                        const uint64_t bdesc = bdesc0 + (uint64_t)(j * (kPfXB >> 4));
+                        const uint32_t d = tmem + b * kPfTok, a = tmem + kPfA0 + (j % kPfAS) * 32;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            pf_mma(d, a + kk * 8, bdesc + (uint64_t)(kk * 2), idesc, (fresh && kk == 0) ? 0u : 1u);
+                        pf_commit(&done[j]);
+                    }
+                    if (j & 1) {
+                        if (++kb == KB)
+                            kb = 0;
+                        if (BITS == 8 && (kb == 0 || i0 + j == steps - 1) && issuer)
+                            pf_commit(&accfull[b]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------- retire warps ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfRegsRetire));
+        pdl_wait(); // y and the workspace may still be in use by the preceding kernel
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const int nch = p.n / 16, ch0 = h == 0 ? 0 : (nch + 1) / 2; // this warp's 16-column chunks
+        const int nc = h == 0 ? (nch + 1) / 2 : nch - (nch + 1) / 2;
+        const int r = 32 * q + lane;
+        const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + 16 * ch0;
+        const uint32_t ebar0 = pf_map(&accempty[0], 0), ebar1 = pf_map(&accempty[1], 0);
+        const int slot_warp = (int)rank * 8 + warp - 4;
+
+        auto owner = [&](int u) { // the pair whose range holds unit u (the last one that starts at or before it)
+            int lo = 0, hi = G - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (start_of(mid) <= u)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            return lo;
+        };
+        auto part_of = [&](int c, int tile) {
+            const int slot = start_of(c) / KB == tile ? 0 : 1;
+            return p.part + ((size_t)((c * 2 + slot) * 2 + (int)rank) * kPfTok + 16 * ch0) * kPanelRows + r;
+        };
+        // Writes the 16 tokens of chunk c of a tile's sums, through the epilogue.
+        auto out16 = [&](int tile, int c, float(&v)[16], float scale) {
+            const int nn = (2 * (tile / p.TT) + (int)rank) * kPanelRows + r;
+            const int m0 = (tile % p.TT) * p.n + 16 * (ch0 + c), jn = min(16, p.M - m0);
+            if (nn < p.N && jn > 0) {
+                if constexpr (BITS == 8) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] *= scale;
+                }
+                epi_store_tokens<true, 16, 16>(p.epi, p.y, p.N, m0, jn, nn, v);
+            }
+        };
+        auto scale_of = [&](int tile) {
+            if constexpr (BITS == 8) {
+                const int nn = (2 * (tile / p.TT) + (int)rank) * kPanelRows + r;
+                return nn < p.N ? bf16_bits_to_float(p.scales[nn]) : 0.f;
+            } else {
+                return 1.f;
+            }
+        };
+        // After this warp stored its partial of a split tile: the ticket; the
+        // last to come adds the partials in the pairs' order and writes y.
+        auto finish_split = [&](int tile) {
+            __threadfence();
+            __syncwarp();
+            const int cf = owner(tile * KB), cl = owner((tile + 1) * KB - 1);
+            uint32_t ticket = 0;
+            if (lane == 0)
+                ticket = ticket_take_acq_rel(&p.cnt[cf * 16 + slot_warp]);
+            ticket = __shfl_sync(0xffffffffu, ticket, 0);
+            if (ticket != (uint32_t)(cl - cf))
+                return;
+            __syncwarp();
+            const float scale = scale_of(tile);
+            for (int c = 0; c < nc; ++c) {
+                float t[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    t[j] = 0.f;
+                for (int cc = cf; cc <= cl; ++cc) {
+                    const float *src = part_of(cc, tile) + (size_t)c * 16 * kPanelRows;
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = __ldcg(src + j * kPanelRows);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        t[j] += v[j];
+                }
+                out16(tile, c, t, scale);
+            }
+            if (lane == 0)
+                atomicExch(&p.cnt[cf * 16 + slot_warp], 0u);
+        };
+
+        // A tile's sums stand in accumulator b: to y, or, for a tile that other
+        // pairs share, to this pair's partial.  The accumulator is released
+        // after the last column is read.
+        auto flush = [&](int tile, int b) {
+            const bool whole = u0 <= tile * KB && u1 >= (tile + 1) * KB;
+            const float scale = scale_of(tile);
+            float *mine = part_of(pair, tile);
+            for (int c = 0; c < nc; ++c) {
+                float v[16];
+                tmem_ld_32x32b_x16(tq + b * kPfTok + 16 * c, v);
+                tmem_wait_ld();
+                if (c == nc - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        pf_arrive(b ? ebar1 : ebar0);
+                }
+                if (whole) {
+                    out16(tile, c, v, scale);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        mine[(size_t)(16 * c + j) * kPanelRows] = v[j];
+                }
+            }
+            if (nc == 0) { // a tile of 16 tokens: the other half has them
+                __syncwarp();
+                if (lane == 0)
+                    pf_arrive(b ? ebar1 : ebar0);
+            }
+            if (!whole)
+                finish_split(tile);
+        };
+
+        if constexpr (BITS == 4) {
+            float tot[kPfChunks * 16];
+#pragma unroll
+            for (int j = 0; j < kPfChunks * 16; ++j)
+                tot[j] = 0.f;
+            int tile = tile0, kb = kb0;
+            for (int g = 0; g < nu; ++g) {
+                const int st = 2 * g + 1, ss = g % kPfSS; // the group's last step
+                if (!mbar_wait_warp(&done[st % kPfXS], (st / kPfXS) & 1) ||
+                    !mbar_wait_warp(&sfull[ss], (g / kPfSS) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float s = bf16_bits_to_float(reinterpret_cast<const uint16_t *>(sS + ss * 256)[r]);
+                const uint32_t ta = tq + (g & 1) * kPfTok;
+#pragma unroll
+                for (int c = 0; c < kPfChunks; c += 2) {
+                    float v[2][16];
+                    if (c < nc)
+                        tmem_ld_32x32b_x16(ta + 16 * c, v[0]);
+                    if (c + 1 < nc)
+                        tmem_ld_32x32b_x16(ta + 16 * c + 16, v[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (c + e < nc)
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2)
+                                pf_ffma2(tot[16 * (c + e) + j], tot[16 * (c + e) + j + 1], s, v[e][j], v[e][j + 1]);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sempty[ss]);
+                const bool end = ++kb == KB;
+                if (!end && g < nu - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        pf_arrive((g & 1) ? ebar1 : ebar0);
+                    continue;
+                }
+                // the tile's (or the run's) last group: the totals take its
+                // accumulator's place, so that writing them out needs few registers
+#pragma unroll
+                for (int c = 0; c < kPfChunks; ++c)
+                    if (c < nc) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = __float_as_uint(tot[16 * c + j]);
+                        tmem_st_32x32b_x16(ta + 16 * c, w);
+                    }
+                tmem_wait_st();
+                flush(tile, g & 1);
+#pragma unroll
+                for (int j = 0; j < kPfChunks * 16; ++j)
+                    tot[j] = 0.f;
+                kb = 0;
+                ++tile;
+            }
+        } else {
+            const int tile1 = nu > 0 ? (u1 - 1) / KB : tile0 - 1;
+            for (int tile = tile0; tile <= tile1; ++tile) {
+                const int t = tile - tile0, b = t & 1;
+                if (!mbar_wait_warp(&accfull[b], (t >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                flush(tile, b);
+            }
+        }
+    } else {
+        // ---------------- dequantization warps ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfRegsDequant));
+        const int q = warp & 3, e = (warp - 12) >> 2;
+        const uint32_t bar = pf_map(full, 0);
+        const int r = 32 * q + lane, g = lane >> 2, blkrow = 2 * q + e; // INT8: this lane's row; INT4: 16-row block
+        const int steps = 2 * nu;
+        // this lane's packed values of a step (the next step's are fetched while
+        // this one is converted and stored)
+        uint4 w[2];
+        int ws = 0;
+        uint32_t wpar = 0;
+        auto fetch = [&](int hf) {
+            const uint8_t *blk = sW + (size_t)ws * WB;
+            if constexpr (BITS == 4) {
+                w[0] = *reinterpret_cast<const uint4 *>(blk + blkrow * 1024 + hf * 512 + lane * 16);
+            } else {
+                const int c = 4 * hf + 2 * e; // two 16-k chunks of one row
+                w[0] = *reinterpret_cast<const uint4 *>(blk + int8_chunk_in_block(r, c));
+                w[1] = *reinterpret_cast<const uint4 *>(blk + int8_chunk_in_block(r, c + 1));
+            }
+        };
+        uint32_t zlo = 0, zhi = 0;
+        auto fetch_zeros = [&]() { // rows 16 blkrow + g and + 8
+            if constexpr (BITS == 4) {
+                const uint8_t *zp = sZ + ws * 128 + 8 * blkrow + (g >> 1);
+                const uint32_t z0 = (zp[0] >> (4 * (g & 1))) & 0xFu, z1 = (zp[4] >> (4 * (g & 1))) & 0xFu;
+                zlo = 0x43004300u | z0 | (z0 << 16);
+                zhi = 0x43004300u | z1 | (z1 << 16);
+            }
+        };
+        ok = mbar_wait_warp(&wfull[0], 0);
+        if (ok)
+            fetch(0);
+        uint32_t par = 1; // of the steps four before, in the second half of each round
+        for (int i0 = 0; i0 < steps && ok; i0 += kPfXS, par ^= 1) {
+#pragma unroll
+            for (int j = 0; j < kPfXS; ++j) {
+                if (i0 + j >= steps)
+                    break;
+                if ((j & 1) == 0)
+                    fetch_zeros();
+                uint32_t rr[16];
+                if constexpr (BITS == 4) {
+                    int4_tile_regs(w[0], zlo, zhi, rr);
+                } else {
+                    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        rr[2 * h] = pf_s8pair(v[h], 0);
+                        rr[2 * h + 1] = pf_s8pair(v[h], 1);
+                    }
+                }
+                if ((j & 1) == 0) {
+                    fetch(1);
+                } else { // every value loaded from the stage has been used: release it, go to the next
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&wempty[ws]);
+                    if (++ws == WS) {
+                        ws = 0;
+                        wpar ^= 1;
+                    }
+                    if (i0 + j + 1 < steps) {
+                        if (!mbar_wait_warp(&wfull[ws], wpar)) {
+                            ok = false;
+                            break;
+                        }
+                        fetch(0);
+                    }
+                }
+                // the stage's last products: step i - 4, in slot (j + 4) % 8
+                if ((i0 > 0 || j >= kPfAS) && !mbar_wait_warp(&done[(j + kPfAS) % kPfXS], j < kPfAS ? par : par ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t ta = tmem + kPfA0 + (j % kPfAS) * 32;
+                if constexpr (BITS == 4)
+                    tmem_st_16x256b_x4(ta + ((uint32_t)(32 * q + 16 * e) << 16), rr);
+                else
+                    tmem_st_32x32b_x16(ta + ((uint32_t)(32 * q) << 16) + 16 * e, rr);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    pf_arrive(bar + j * 8);
+            }
+        }
+    }
+
+    if (!ok)
+        atomicExch(&g_gemm_pf_error, kErrTimeout);
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    pf_cluster_sync(); // neither CTA leaves while the other may still signal it
+    if (warp == 2) {
+        tc_fence_after();
+        pf_tmem_dealloc(tmem);
+    }
+}
+
+bool pf_x_map(CUtensorMap *map, const uint16_t *x, int M, int K, int rows)
+{
+    auto fn = get_encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M};
+    const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(x), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BITS>
+cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+{
+    constexpr size_t smem = pf_smem_bytes<BITS>();
+    static_assert(smem <= 227 * 1024, "shared memory per CTA");
+    cudaError_t e = kernel_setup((const void *)gemm_pf_kernel<BITS>, smem, 0, 0, nullptr);
+    if (e != cudaSuccess)
+        return e;
+    // the warps' shares after setmaxnreg must fit what the CTA is launched with,
+    // or the retire warps would wait for registers that never come
+    static int regs = 0; // the same on every device
+    if (regs == 0) {
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, (const void *)gemm_pf_kernel<BITS>)) != cudaSuccess)
+            return e;
+        regs = fa.numRegs;
+    }
+    if (regs * kPfThreads < 128 * kPfRegsIssue + 256 * kPfRegsRetire + 256 * kPfRegsDequant)
+        return cudaErrorInvalidConfiguration;
+    const Shape sh{a.bits, a.K, a.N, a.group};
+    PfParams p;
+    p.M = a.M;
+    p.N = a.N;
+    p.KB = sh.kblocks();
+    p.panels = sh.panels();
+    p.TT = (a.M + kPfTok - 1) / kPfTok;
+    p.n = ((a.M + p.TT - 1) / p.TT + 15) / 16 * 16;
+    p.TT = (a.M + p.n - 1) / p.n;
+    const long long tiles = (long long)((p.panels + 1) / 2) * p.TT, units = tiles * p.KB;
+    if (units >= (1LL << 31))
+        return cudaErrorInvalidValue; // the caller cuts M (pf_max_tokens)
+    p.tiles = (int)tiles;
+    p.U = (int)units;
+    p.wq = (const uint8_t *)a.wq;
+    p.scales = (const uint16_t *)a.scales;
+    p.zeros = (const uint8_t *)a.zeros;
+    p.y = a.y;
+    p.epi = *a.epi;
+    p.cnt = (uint32_t *)ws;
+    p.part = ws ? (float *)((uint8_t *)ws + ws_counter_bytes()) : nullptr;
+    p.align = ws ? 0 : 1;
+    const int pairs = sm_count / 2 < kPfMaxPairs ? sm_count / 2 : kPfMaxPairs;
+    // at least four units a pair: a tile's sums are not cut finer than 512 k
+    const long long want = ws ? (units + 3) / 4 : tiles;
+    const long long most = want > tiles ? want : tiles;
+    const int G = (int)(most < pairs ? most : pairs);
+    CUtensorMap map;
+    if (!pf_x_map(&map, a.x, a.M, a.K, p.n / 2))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2 * G);
+    cfg.blockDim = dim3(kPfThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, gemm_pf_kernel<BITS>, map, p);
+}
+
+} // namespace
+
+size_t ws_bytes_gemm_pf() { return ws_counter_bytes() + (size_t)kPfMaxPairs * 4 * kPfTok * kPanelRows * sizeof(float); }
+
+// Tokens of one launch: its units stay below 2^31.
+int pf_max_tokens(int K, int N)
+{
+    const long long per_tile = (long long)((N + 255) / 256) * ((K + kBlockK - 1) / kBlockK);
+    const long long t = ((1LL << 31) - 1) / per_tile * kPfTok;
+    return t > kMaxTokens ? kMaxTokens : (int)t;
+}
+
+cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+{
+    return a.bits == 8 ? launch_pf_t<8>(a, ws, sm_count, st) : launch_pf_t<4>(a, ws, sm_count, st);
+}
+
+cudaError_t read_gemm_pf_error(int *code, cudaStream_t st)
+{
+    int host = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&host, g_gemm_pf_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+    if (e != cudaSuccess)
+        return e;
+    e = cudaMemcpyToSymbolAsync(g_gemm_pf_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+    if (e != cudaSuccess)
+        return e;
+    e = cudaStreamSynchronize(st);
+    *code = host;
+    return e;
+}
+
+} // namespace wq

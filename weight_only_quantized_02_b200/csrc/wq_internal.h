@@ -126,6 +126,15 @@ size_t ws_bytes_gemm_i4(int M, int K, int N);
 cudaError_t launch_gemm_i4(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st);
 cudaError_t read_gemm_i4_error(int *code, cudaStream_t st);
 
+// Prompt GEMM on pairs of SMs (W8A16 and W4A16 of layout group 128), with an
+// epilogue (a.epi): any M up to pf_max_tokens; ws >= ws_bytes_gemm_pf(), or
+// NULL (no split tiles).
+constexpr int kPfMaxPairs = 80;
+size_t ws_bytes_gemm_pf();
+int pf_max_tokens(int K, int N);
+cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st);
+cudaError_t read_gemm_pf_error(int *code, cudaStream_t st);
+
 // Integer GEMV (mma.sync m16n8k32 on the packed codes): M <= kGiMaxM,
 // K <= kI8MaxK, the 16-warp CTA's dynamic shared memory (digit rows, INT4
 // digit sums, stash of partial sums: gi_smem_bytes) at most kGiMaxSmem;
