@@ -53,20 +53,42 @@ __device__ __forceinline__ uint16_t float_to_act16(float v)
         return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// Out of line: five formulas inlined at every output of the unrolled stores
-// would multiply the kernels' code.  The erf form is written with erfc, which
-// keeps its relative accuracy where 1 + erf cancels; the tanh form is
-// v * logistic(2 u), which does not cancel either.
+// The activation of CNT values.  The erf form is written with erfc, which keeps
+// its relative accuracy where 1 + erf cancels; the tanh form is v * logistic(2 u),
+// which does not cancel either.  The logistic function uses the fast exponential
+// and division (a few 2^-22 of its value more per unit of |u|), against an output
+// of 8 or 11 significant bits.
+template <int CNT>
+__device__ __forceinline__ void epi_activations(float (&v)[CNT], int act)
+{
+    if (act == WQ_ACT_NONE)
+        return;
+    if (act == WQ_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < CNT; ++j)
+            v[j] = v[j] < 0.f ? 0.f : v[j];
+    } else if (act == WQ_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < CNT; ++j)
+            v[j] = 0.5f * v[j] * erfcf(-0.70710678f * v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < CNT; ++j) {
+            float u = v[j]; // WQ_ACT_SILU: v * logistic(v)
+            if (act == WQ_ACT_GELU_TANH)
+                u = 1.5957691f * fmaf(0.044715f * u, u * u, u); // 2 sqrt(2/pi) (v + 0.044715 v^3)
+            v[j] = __fdividef(v[j], 1.f + __expf(-u));
+        }
+    }
+}
+
+// One value, out of line: the formulas inlined at every output of the unrolled
+// stores would multiply the kernels' code.
 static __device__ __noinline__ float epi_activation(float v, int act)
 {
-    if (act == WQ_ACT_RELU)
-        return v < 0.f ? 0.f : v;
-    if (act == WQ_ACT_GELU)
-        return 0.5f * v * erfcf(-0.70710678f * v);
-    float u = v; // WQ_ACT_SILU: v * logistic(v)
-    if (act == WQ_ACT_GELU_TANH)
-        u = 1.5957691f * fmaf(0.044715f * v, v * v, v); // 2 sqrt(2/pi) (v + 0.044715 v^3)
-    return v / (1.f + expf(-u));
+    float x[1] = {v};
+    epi_activations(x, act);
+    return x[0];
 }
 
 // The operands of output (m, n); absent ones are the identity.

@@ -61,6 +61,7 @@ constexpr int kPfAS = 4;      // A stages (64 k, 32 columns)
 constexpr int kPfXS = 8;      // x stages (64 k); also the steps' barriers: operands complete, products done
 constexpr int kPfSS = 16;     // scale stages
 constexpr int kPfXB = kPfTok / 2 * 128; // bytes of an x stage
+constexpr int kPfOutB = 16 * kPanelRows * 4; // 16 tokens of a CTA's channels on their way out, fp32
 constexpr int kPfChunks = kPfTok / 32;  // 16-column chunks of a retire warp, at most
 static_assert(kPfA0 + kPfAS * 32 == 512, "tensor memory plan");
 static_assert(kPfXS == 8 && kPfXS >= kPfAS, "a step's barriers are read before their slot comes round (two groups are four steps)");
@@ -68,7 +69,7 @@ static_assert(kPfXS == 8 && kPfXS >= kPfAS, "a step's barriers are read before t
 template <int BITS>
 struct PfCfg {
     static constexpr int kWB = BITS == 4 ? 8192 : 16384;
-    static constexpr int kWS = BITS == 4 ? 8 : 6;
+    static constexpr int kWS = BITS == 4 ? 8 : 5;
 };
 
 struct PfParams {
@@ -80,14 +81,15 @@ struct PfParams {
     uint16_t *y;
     EpiArgs epi;
     float *part;   // [pairs][2 slots][2 CTAs][kPfTok tokens][128 rows]
-    uint32_t *cnt; // [pairs][2 CTAs][8 warps], by a split tile's first pair
+    uint32_t *cnt; // [pairs][2 CTAs][2 halves], by a split tile's first pair
 };
 
 template <int BITS>
 constexpr size_t pf_smem_bytes()
 {
     using C = PfCfg<BITS>;
-    return 1024 + (size_t)kPfXS * kPfXB + (size_t)C::kWS * C::kWB + (size_t)kPfSS * 256 + (size_t)C::kWS * 128 +
+    return 1024 + (size_t)kPfXS * kPfXB + (size_t)C::kWS * C::kWB + 4 * kPfOutB + (size_t)kPfSS * 256 +
+           (size_t)C::kWS * 128 +
            (size_t)(2 * kPfXS + 2 * C::kWS + 2 * kPfSS + 4) * 8 + 16;
 }
 
@@ -110,6 +112,19 @@ __device__ __forceinline__ uint32_t pf_map(const void *p, uint32_t rank)
 __device__ __forceinline__ void pf_arrive(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// Barrier of the four warps of one half of the retire warps, and whether all of
+// them are well.
+__device__ __forceinline__ bool pf_all(int id, bool ok)
+{
+    uint32_t r;
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+                 "barrier.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"(128), "r"((uint32_t)ok)
+                 : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ bool pf_elect() // one lane of the (converged) warp
 {
@@ -178,9 +193,246 @@ __device__ __forceinline__ uint32_t pf_s8pair(uint32_t w, int h)
     return bf16x2_sub(mag, off);
 }
 
+// First unit of pair c.
+__device__ __forceinline__ int pf_start(const PfParams &p, int G, int c)
+{
+    return p.align ? sk_start(p.tiles, G, c) * p.KB : sk_start(p.U, G, c);
+}
+
+// The pair whose range holds unit u: the last one that starts at or before it.
+__device__ __forceinline__ int pf_owner(const PfParams &p, int G, int u)
+{
+    int lo = 0, hi = G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pf_start(p, G, mid) <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// What a retire warp needs to write a tile out.
+struct PfRetire {
+    int ch0, nc; // the warp's half: first 16-token chunk of a tile, chunks
+    int G, pair, rank, u0, u1;
+    float *obuf;      // the half's two output buffers
+    uint32_t *ticket; // the half's shared word
+    uint32_t ebar;    // the leader's accempty barriers
+    uint32_t tq;      // the warp's corner of accumulator 0
+};
+
+// The output path: 16 tokens (a chunk) of the CTA's 128 channels at a time.  The
+// half's four warps put their sums into shared memory, a channel a thread, and
+// take them out as 8 consecutive channels of a token a thread, so that y and
+// the operands move in 16-byte pieces, 256 contiguous bytes a token.  (Written
+// 2 bytes a lane, 64 a warp, a tile with a residual took 38 us to leave.)
+struct PfOut {
+    const PfParams &p;
+    const PfRetire &rt;
+    int tile, nn0, og, ot, r, id, ob;
+    bool vec_mul, vec_res;
+    uint4 mul[2], res[2]; // the operands of this thread's two tokens of the next chunk
+
+    __device__ __forceinline__ PfOut(const PfParams &p_, const PfRetire &rt_, int tile_) : p(p_), rt(rt_), tile(tile_)
+    {
+        const int t128 = threadIdx.x & 127;
+        og = 8 * (t128 & 15);
+        ot = t128 >> 4;
+        r = t128; // warps 4-7 and 8-11: lane quadrant warp % 4
+        id = 1 + ((threadIdx.x - 128) >> 7);
+        ob = 0; // the half has met since the buffers were last read
+        nn0 = (2 * (tile / p.TT) + rt.rank) * kPanelRows;
+        vec_mul = ((reinterpret_cast<uintptr_t>(p.epi.mul) | (uintptr_t)(2 * p.epi.ld_mul)) & 15) == 0;
+        vec_res = ((reinterpret_cast<uintptr_t>(p.epi.res) | (uintptr_t)(2 * p.epi.ld_res)) & 15) == 0;
+    }
+
+    __device__ __forceinline__ int token(int c) const { return (tile % p.TT) * p.n + 16 * (rt.ch0 + c) + ot; }
+
+    static __device__ __forceinline__ uint4 row8(const uint16_t *src, bool vec)
+    {
+        if (vec)
+            return __ldcg(reinterpret_cast<const uint4 *>(src));
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = (uint32_t)__ldcg(src + 2 * j) | ((uint32_t)__ldcg(src + 2 * j + 1) << 16);
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+
+    // Fetches the operands of chunk c.
+    __device__ __forceinline__ void fetch(int c)
+    {
+        const int nn = nn0 + og, m0 = token(c);
+        if (nn >= p.N || c >= rt.nc)
+            return;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = m0 + 8 * e;
+            if (m < p.M && p.epi.mul)
+                mul[e] = row8(p.epi.mul + (long long)m * p.epi.ld_mul + nn, vec_mul);
+            if (m < p.M && p.epi.res)
+                res[e] = row8(p.epi.res + (long long)m * p.epi.ld_res + nn, vec_res);
+        }
+    }
+
+    // Chunk c from this thread's 16 sums (channel r) to y, its operands fetched
+    // before; fetches the next chunk's.
+    __device__ __forceinline__ void emit(int c, const float (&v)[16])
+    {
+        float *buf = rt.obuf + ob * (kPfOutB / 4);
+        ob ^= 1; // a buffer is written again after the other one's barrier: its readers are through
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            buf[j * kPanelRows + r] = v[j];
+        named_barrier_sync(id, 128);
+        const uint4 cm[2] = {mul[0], mul[1]}, cr[2] = {res[0], res[1]};
+        fetch(c + 1);
+        const int nn = nn0 + og, m0 = token(c);
+        if (nn >= p.N)
+            return;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = m0 + 8 * e;
+            if (m >= p.M)
+                break;
+            const float4 a = *reinterpret_cast<const float4 *>(buf + (ot + 8 * e) * kPanelRows + og);
+            const float4 b = *reinterpret_cast<const float4 *>(buf + (ot + 8 * e) * kPanelRows + og + 4);
+            const size_t at = (size_t)m * p.N + nn;
+            if (p.epi.out_f32) {
+                float4 *yp = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.y) + at);
+                yp[0] = a;
+                yp[1] = b;
+                continue;
+            }
+            float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            if (p.epi.bias)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] += act16_to_float<false>(__ldg(p.epi.bias + nn + j));
+            epi_activations(x, p.epi.act);
+            const uint32_t mw[4] = {cm[e].x, cm[e].y, cm[e].z, cm[e].w};
+            const uint32_t rw[4] = {cr[e].x, cr[e].y, cr[e].z, cr[e].w};
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                EpiOps lo{1.f, 0.f}, hi{1.f, 0.f};
+                if (p.epi.mul) {
+                    lo.mul = __uint_as_float(mw[j] << 16);
+                    hi.mul = __uint_as_float(mw[j] & 0xFFFF0000u);
+                }
+                if (p.epi.res) {
+                    lo.res = __uint_as_float(rw[j] << 16);
+                    hi.res = __uint_as_float(rw[j] & 0xFFFF0000u);
+                }
+                const __nv_bfloat162 q2 =
+                    __floats2bfloat162_rn(fmaf(x[2 * j], lo.mul, lo.res), fmaf(x[2 * j + 1], hi.mul, hi.res));
+                w[j] = *reinterpret_cast<const uint32_t *>(&q2);
+            }
+            *reinterpret_cast<uint4 *>(p.y + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+};
+
+// A tile's sums stand in accumulator b: to y, or, for a tile that other pairs
+// share, to this pair's partial and, by the last of them to come (a ticket for
+// each CTA's half), added in the pairs' order to y.  The accumulator is released
+// after its last column is read.  Called by the four warps of a half together.
+// Out of line, so that the retire loop keeps its registers.
+template <int BITS>
+__device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int tile, int b)
+{
+    const int KB = p.KB, lane = threadIdx.x & 31;
+    const bool whole = rt.u0 <= tile * KB && rt.u1 >= (tile + 1) * KB;
+    PfOut out(p, rt, tile);
+    float scale = 1.f;
+    if (BITS == 8 && out.nn0 + out.r < p.N)
+        scale = bf16_bits_to_float(p.scales[out.nn0 + out.r]);
+    auto part_of = [&](int c) { // pair c's partial of this tile
+        const int slot = pf_start(p, rt.G, c) / KB == tile ? 0 : 1;
+        return p.part + ((size_t)((c * 2 + slot) * 2 + rt.rank) * kPfTok + 16 * rt.ch0) * kPanelRows + out.r;
+    };
+    float *mine = part_of(rt.pair);
+    if (whole)
+        out.fetch(0);
+    for (int c = 0; c < rt.nc; ++c) {
+        float v[16];
+        tmem_ld_32x32b_x16(rt.tq + b * kPfTok + 16 * c, v);
+        tmem_wait_ld();
+        if (c == rt.nc - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                pf_arrive(rt.ebar + b * 8);
+        }
+        if (whole) {
+            if constexpr (BITS == 8)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] *= scale;
+            out.emit(c, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                mine[(size_t)(16 * c + j) * kPanelRows] = v[j];
+        }
+    }
+    if (rt.nc == 0) { // a tile of 16 tokens: the other half has them
+        __syncwarp();
+        if (lane == 0)
+            pf_arrive(rt.ebar + b * 8);
+    }
+    if (whole)
+        return;
+    const int cf = pf_owner(p, rt.G, tile * KB), cl = pf_owner(p, rt.G, (tile + 1) * KB - 1);
+    uint32_t *counter = p.cnt + cf * 4 + rt.rank * 2 + out.id - 1;
+    __threadfence();
+    named_barrier_sync(out.id, 128);
+    if (out.r == 0)
+        *rt.ticket = ticket_take_acq_rel(counter);
+    named_barrier_sync(out.id, 128);
+    const bool last = *rt.ticket == (uint32_t)(cl - cf);
+    named_barrier_sync(out.id, 128); // read before the next ticket is written
+    if (!last)
+        return;
+    __threadfence();
+    out.fetch(0);
+    for (int c = 0; c < rt.nc; ++c) {
+        float t[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            t[j] = 0.f;
+        for (int cc = cf; cc <= cl; cc += 2) { // two contributors' loads in flight, added in order
+            float v[2][16];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (cc + e <= cl) {
+                    const float *src = part_of(cc + e) + (size_t)c * 16 * kPanelRows;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[e][j] = __ldcg(src + j * kPanelRows);
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (cc + e <= cl)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        t[j] += v[e][j];
+        }
+        if constexpr (BITS == 8)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                t[j] *= scale;
+        out.emit(c, t);
+    }
+    if (out.r == 0)
+        atomicExch(counter, 0u); // ready for the next call
+}
+
 template <int BITS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
-    gemm_pf_kernel(const __grid_constant__ CUtensorMap tmx, const PfParams p)
+    gemm_pf_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ PfParams p)
 {
     using C = PfCfg<BITS>;
     constexpr int WS = C::kWS, WB = C::kWB;
@@ -188,7 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sX = smem;                // kPfXS x stages, 1024-byte aligned
     uint8_t *sW = sX + kPfXS * kPfXB;  // WS packed blocks
-    uint8_t *sS = sW + (size_t)WS * WB; // kPfSS group scales
+    uint8_t *sO = sW + (size_t)WS * WB; // two output buffers for each half of the retire warps
+    uint8_t *sS = sO + 4 * kPfOutB;     // kPfSS group scales
     uint8_t *sZ = sS + kPfSS * 256;    // WS zero points
     uint64_t *full = reinterpret_cast<uint64_t *>(sZ + WS * 128);
     uint64_t *done = full + kPfXS;
@@ -196,15 +449,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     uint64_t *sfull = wempty + WS, *sempty = sfull + kPfSS;
     uint64_t *accfull = sempty + kPfSS, *accempty = accfull + 2;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(accempty + 2);
+    uint32_t *s_ticket = s_tmem + 1; // [2 halves]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = pf_rank();
     const int G = gridDim.x >> 1, pair = blockIdx.x >> 1, KB = p.KB;
     // this pair's units [u0, u1)
-    auto start_of = [&](int c) {
-        return p.align ? sk_start(p.tiles, G, c) * KB : sk_start(p.U, G, c);
-    };
-    const int u0 = start_of(pair), u1 = start_of(pair + 1), nu = u1 - u0;
+    const int u0 = pf_start(p, G, pair), u1 = pf_start(p, G, pair + 1), nu = u1 - u0;
     const int tile0 = u0 / KB, kb0 = u0 % KB;
 
     if (threadIdx.x == 0) {
@@ -368,117 +619,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfRegsRetire));
         pdl_wait(); // y and the workspace may still be in use by the preceding kernel
         const int q = warp & 3, h = (warp - 4) >> 2;
-        const int nch = p.n / 16, ch0 = h == 0 ? 0 : (nch + 1) / 2; // this warp's 16-column chunks
-        const int nc = h == 0 ? (nch + 1) / 2 : nch - (nch + 1) / 2;
-        const int r = 32 * q + lane;
-        const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + 16 * ch0;
-        const uint32_t ebar0 = pf_map(&accempty[0], 0), ebar1 = pf_map(&accempty[1], 0);
-        const int slot_warp = (int)rank * 8 + warp - 4;
-
-        auto owner = [&](int u) { // the pair whose range holds unit u (the last one that starts at or before it)
-            int lo = 0, hi = G - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (start_of(mid) <= u)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
-            return lo;
-        };
-        auto part_of = [&](int c, int tile) {
-            const int slot = start_of(c) / KB == tile ? 0 : 1;
-            return p.part + ((size_t)((c * 2 + slot) * 2 + (int)rank) * kPfTok + 16 * ch0) * kPanelRows + r;
-        };
-        // Writes the 16 tokens of chunk c of a tile's sums, through the epilogue.
-        auto out16 = [&](int tile, int c, float(&v)[16], float scale) {
-            const int nn = (2 * (tile / p.TT) + (int)rank) * kPanelRows + r;
-            const int m0 = (tile % p.TT) * p.n + 16 * (ch0 + c), jn = min(16, p.M - m0);
-            if (nn < p.N && jn > 0) {
-                if constexpr (BITS == 8) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[j] *= scale;
-                }
-                epi_store_tokens<true, 16, 16>(p.epi, p.y, p.N, m0, jn, nn, v);
-            }
-        };
-        auto scale_of = [&](int tile) {
-            if constexpr (BITS == 8) {
-                const int nn = (2 * (tile / p.TT) + (int)rank) * kPanelRows + r;
-                return nn < p.N ? bf16_bits_to_float(p.scales[nn]) : 0.f;
-            } else {
-                return 1.f;
-            }
-        };
-        // After this warp stored its partial of a split tile: the ticket; the
-        // last to come adds the partials in the pairs' order and writes y.
-        auto finish_split = [&](int tile) {
-            __threadfence();
-            __syncwarp();
-            const int cf = owner(tile * KB), cl = owner((tile + 1) * KB - 1);
-            uint32_t ticket = 0;
-            if (lane == 0)
-                ticket = ticket_take_acq_rel(&p.cnt[cf * 16 + slot_warp]);
-            ticket = __shfl_sync(0xffffffffu, ticket, 0);
-            if (ticket != (uint32_t)(cl - cf))
-                return;
-            __syncwarp();
-            const float scale = scale_of(tile);
-            for (int c = 0; c < nc; ++c) {
-                float t[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    t[j] = 0.f;
-                for (int cc = cf; cc <= cl; ++cc) {
-                    const float *src = part_of(cc, tile) + (size_t)c * 16 * kPanelRows;
-                    float v[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[j] = __ldcg(src + j * kPanelRows);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        t[j] += v[j];
-                }
-                out16(tile, c, t, scale);
-            }
-            if (lane == 0)
-                atomicExch(&p.cnt[cf * 16 + slot_warp], 0u);
-        };
-
-        // A tile's sums stand in accumulator b: to y, or, for a tile that other
-        // pairs share, to this pair's partial.  The accumulator is released
-        // after the last column is read.
-        auto flush = [&](int tile, int b) {
-            const bool whole = u0 <= tile * KB && u1 >= (tile + 1) * KB;
-            const float scale = scale_of(tile);
-            float *mine = part_of(pair, tile);
-            for (int c = 0; c < nc; ++c) {
-                float v[16];
-                tmem_ld_32x32b_x16(tq + b * kPfTok + 16 * c, v);
-                tmem_wait_ld();
-                if (c == nc - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        pf_arrive(b ? ebar1 : ebar0);
-                }
-                if (whole) {
-                    out16(tile, c, v, scale);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        mine[(size_t)(16 * c + j) * kPanelRows] = v[j];
-                }
-            }
-            if (nc == 0) { // a tile of 16 tokens: the other half has them
-                __syncwarp();
-                if (lane == 0)
-                    pf_arrive(b ? ebar1 : ebar0);
-            }
-            if (!whole)
-                finish_split(tile);
-        };
+        const int nch = p.n / 16;
+        PfRetire rt;
+        rt.ch0 = h == 0 ? 0 : (nch + 1) / 2; // this warp's 16-column chunks
+        rt.nc = h == 0 ? (nch + 1) / 2 : nch - (nch + 1) / 2;
+        rt.G = G;
+        rt.pair = pair;
+        rt.rank = (int)rank;
+        rt.u0 = u0;
+        rt.u1 = u1;
+        rt.obuf = reinterpret_cast<float *>(sO) + h * 2 * (kPfOutB / 4);
+        rt.ticket = s_ticket + h;
+        rt.ebar = pf_map(accempty, 0);
+        rt.tq = tmem + ((uint32_t)(32 * q) << 16) + 16 * rt.ch0;
+        const int r = 32 * q + lane, nc = rt.nc;
+        const uint32_t tq = rt.tq;
 
         if constexpr (BITS == 4) {
             float tot[kPfChunks * 16];
@@ -488,29 +643,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             int tile = tile0, kb = kb0;
             for (int g = 0; g < nu; ++g) {
                 const int st = 2 * g + 1, ss = g % kPfSS; // the group's last step
-                if (!mbar_wait_warp(&done[st % kPfXS], (st / kPfXS) & 1) ||
-                    !mbar_wait_warp(&sfull[ss], (g / kPfSS) & 1)) {
-                    ok = false;
-                    break;
-                }
+                // A warp whose wait gave up goes on without waiting, so that every
+                // warp of the half comes to the barriers of every tile.
+                ok = ok && mbar_wait_warp(&done[st % kPfXS], (st / kPfXS) & 1) &&
+                     mbar_wait_warp(&sfull[ss], (g / kPfSS) & 1);
                 tc_fence_after();
                 const float s = bf16_bits_to_float(reinterpret_cast<const uint16_t *>(sS + ss * 256)[r]);
                 const uint32_t ta = tq + (g & 1) * kPfTok;
 #pragma unroll
-                for (int c = 0; c < kPfChunks; c += 2) {
-                    float v[2][16];
-                    if (c < nc)
-                        tmem_ld_32x32b_x16(ta + 16 * c, v[0]);
-                    if (c + 1 < nc)
-                        tmem_ld_32x32b_x16(ta + 16 * c + 16, v[1]);
-                    tmem_wait_ld();
+                for (int c = 0; c < kPfChunks; ++c) // 16 columns at a time: 32 would spill
+                    if (c < nc) {
+                        float v[16];
+                        tmem_ld_32x32b_x16(ta + 16 * c, v);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (c + e < nc)
-#pragma unroll
-                            for (int j = 0; j < 16; j += 2)
-                                pf_ffma2(tot[16 * (c + e) + j], tot[16 * (c + e) + j + 1], s, v[e][j], v[e][j + 1]);
-                }
+                        for (int j = 0; j < 16; j += 2)
+                            pf_ffma2(tot[16 * c + j], tot[16 * c + j + 1], s, v[j], v[j + 1]);
+                    }
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&sempty[ss]);
@@ -519,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        pf_arrive((g & 1) ? ebar1 : ebar0);
+                        pf_arrive(rt.ebar + (g & 1) * 8);
                     continue;
                 }
                 // the tile's (or the run's) last group: the totals take its
@@ -534,7 +683,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         tmem_st_32x32b_x16(ta + 16 * c, w);
                     }
                 tmem_wait_st();
-                flush(tile, g & 1);
+                ok = pf_all(1 + h, ok);
+                if (ok)
+                    pf_flush<BITS>(p, rt, tile, g & 1);
 #pragma unroll
                 for (int j = 0; j < kPfChunks * 16; ++j)
                     tot[j] = 0.f;
@@ -545,12 +696,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             const int tile1 = nu > 0 ? (u1 - 1) / KB : tile0 - 1;
             for (int tile = tile0; tile <= tile1; ++tile) {
                 const int t = tile - tile0, b = t & 1;
-                if (!mbar_wait_warp(&accfull[b], (t >> 1) & 1)) {
-                    ok = false;
-                    break;
-                }
+                ok = pf_all(1 + h, ok && mbar_wait_warp(&accfull[b], (t >> 1) & 1));
+                if (!ok)
+                    break; // the whole half
                 tc_fence_after();
-                flush(tile, b);
+                pf_flush<BITS>(p, rt, tile, b);
             }
         }
     } else {
