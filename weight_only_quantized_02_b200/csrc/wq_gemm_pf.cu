@@ -9,36 +9,40 @@
 // the epilogue is the fp32 accumulation.
 //
 // Bound: the tensor cores.  Two CTAs (a cluster, one on each SM of a pair)
-// work on one tile of 256 output channels x up to 192 tokens with
-// tcgen05.mma.cta_group::2: each CTA holds its own 128 channels' weights and
-// accumulators in its tensor memory and half of the tokens' activations in
-// its shared memory, so an activation byte is brought in once for 256
-// channels.  A CTA alone (128 x 192) would have to fill 48 KB of activations
-// per 128 k, more than L2 gives an SM in the time of its products.
+// work on one tile of 256 output channels with tcgen05.mma.cta_group::2: each
+// CTA holds its own 128 channels' weights and accumulators in its tensor memory
+// and half of the tokens' activations in its shared memory, so an activation
+// byte is brought in once for 256 channels.  A CTA alone (128 channels) would
+// have to fill twice that, more than L2 gives an SM in the time of its products.
 //
-// A step is 64 k of a tile: four MMAs of K = 16.  Tensor memory: two
-// accumulators of 192 columns (INT4: a group's sums, retired into fp32
-// register totals while the next group is multiplied; INT8: a whole tile's
-// sums, written out while the next tile is multiplied) and four A stages of 32
-// columns.  The token tile is M cut into equal parts of at most 192, rounded
-// up to 16, so ragged prompts waste little.
+// Tensor memory: two accumulators of 192 columns (tokens) and two A stages of
+// 64 columns (128 k of dequantized weights).
+//   INT4: a tile is one accumulator's 192 tokens; a group's sums are retired
+//         into fp32 register totals while the next group is multiplied into the
+//         other accumulator.
+//   INT8: a tile is both accumulators, 384 tokens, so that a dequantized block
+//         is multiplied twice: at 192 tokens the dequantization, some 600
+//         cycles a 64-k step against 384 of products, held the tensor cores back.
+// M is cut into equal tiles, rounded up to 16 tokens, so ragged prompts waste
+// little.
 //
 // Work: units (tile, 128-k block), tiles of one channel panel pair next to each
 // other; each pair of CTAs takes an equal contiguous run of units (stream-K,
 // the partial sums of a tile that two or more pairs share are added in their
 // order by the last to arrive), or whole tiles where there is no workspace.
 //
-// Warps (640 threads; registers are moved to the retire warps):
-//   0      x producer: the CTA's half of the token tile, 64 k a step (tensor
+// Warps (INT4 24, INT8 20; registers are moved to the roles that need them):
+//   0      x producer: the CTA's half of the tile's tokens, 64 k a stage (tensor
 //          map, 128-byte swizzle), signalled on the leader's barrier
 //   1      weight producer: a unit's packed block (and zero points, scales)
-//   2      tensor memory; in the leader CTA, the thread that issues the MMAs
-//   4-11   retire warps: lane quadrant x half of the token columns
-//   12-19  dequantization: packed block -> exact integers in tensor memory
-// One commit per step, to both CTAs, tells the x producers (8 stages), the
-// dequantization (4) and, for INT4, the retire warps (2 groups) that the step
-// is done.  Every wait is bounded (2 s); a timeout is recorded and every role
-// winds down.
+//   2      tensor memory; in the leader CTA, the lane that issues the MMAs
+//   4-15   (INT8: 4-11) retire warps: lane quadrant x a third (half) of the
+//          token columns
+//   the last eight   dequantization: packed block -> exact integers in tensor memory
+// One commit for each 64 k, to both CTAs, tells the x producers (8 or 4 stages),
+// the dequantization (2 units) and, for INT4, the retire warps (2 groups) that
+// the products are done.  Every wait is bounded (2 s); a timeout is recorded and
+// every role winds down.
 #include <cstdint>
 
 #include "wq.h"
@@ -53,44 +57,56 @@ static __device__ int g_gemm_pf_error = 0;
 
 namespace {
 
-constexpr int kPfThreads = 640;
-constexpr int kPfRegsIssue = 32, kPfRegsRetire = 168, kPfRegsDequant = 56; // registers a thread, by role
-constexpr int kPfTok = 192;   // columns of an accumulator
+constexpr int kPfTok = 192;       // columns of an accumulator
 constexpr int kPfA0 = 2 * kPfTok; // first A column
-constexpr int kPfAS = 4;      // A stages (64 k, 32 columns)
-constexpr int kPfXS = 8;      // x stages (64 k); also the steps' barriers: operands complete, products done
-constexpr int kPfSS = 16;     // scale stages
-constexpr int kPfXB = kPfTok / 2 * 128; // bytes of an x stage
-constexpr int kPfOutB = 16 * kPanelRows * 4; // 16 tokens of a CTA's channels on their way out, fp32
-constexpr int kPfChunks = kPfTok / 32;  // 16-column chunks of a retire warp, at most
-static_assert(kPfA0 + kPfAS * 32 == 512, "tensor memory plan");
-static_assert(kPfXS == 8 && kPfXS >= kPfAS, "a step's barriers are read before their slot comes round (two groups are four steps)");
+constexpr int kPfSS = 16;         // scale stages
+constexpr int kPfSplitUnits = 8;
+constexpr int kPfXB = kPfTok / 2 * 128;       // bytes of 64 k of an accumulator's tokens, one CTA's half
+constexpr int kPfOutB = 16 * kPanelRows * 4;  // 16 tokens of a CTA's channels on their way out, fp32
+static_assert(kPfA0 + 2 * 64 == 512, "tensor memory plan");
 
 template <int BITS>
 struct PfCfg {
     static constexpr int kWB = BITS == 4 ? 8192 : 16384;
-    static constexpr int kWS = BITS == 4 ? 8 : 5;
+    static constexpr int kWS = BITS == 4 ? 8 : 4;   // weight stages (units)
+    static constexpr int kSub = BITS == 4 ? 1 : 2;  // accumulators of a tile
+    static constexpr int kXS = 8 / kSub;            // x stages (64 k)
+    static constexpr int kUnroll = kXS / 2;         // units of one round of the x ring
+    static constexpr int kXB = kSub * kPfXB;
+    static constexpr int kAH = kSub;          // 64-k halves of an A stage (32 columns each)
+    static constexpr int kAS = 4 / kAH;       // A stages
+    // retire warps: groups of four (one a lane quadrant) that share an
+    // accumulator's columns
+    static constexpr int kGroups = 2;
+    static constexpr int kChunks = kPfTok / 16 / kGroups; // 16-column chunks of one, at most
+    static constexpr int kThreads = 128 + kGroups * 128 + 256;
+    // registers a thread at launch, and by role
+    static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
+    static constexpr int kRegsIssue = 32, kRegsRetire = BITS == 4 ? 168 : 128,
+                         kRegsDequant = BITS == 4 ? 56 : 80;
+    static constexpr int kRegs = 128 * kRegsIssue + kGroups * 128 * kRegsRetire + 256 * kRegsDequant;
+    static_assert(kRegs <= kThreads * kRegsLaunch, "the roles' registers come out of the CTA's at launch");
+    static_assert(kUnroll % 2 == 0, "a unit's A stage and accumulator are constants of the unrolled loops");
 };
 
 struct PfParams {
-    int M, N, KB, U, TT, n, tiles, panels; // n: tokens of a tile (a multiple of 16)
+    int M, N, KB, U, TT, n, nsub, tiles, panels; // n: tokens of an accumulator (a multiple of 16); nsub of them a tile
     int align;                             // 1: whole tiles per pair
     const uint8_t *wq;
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
     EpiArgs epi;
-    float *part;   // [pairs][2 slots][2 CTAs][kPfTok tokens][128 rows]
-    uint32_t *cnt; // [pairs][2 CTAs][2 halves], by a split tile's first pair
+    float *part;   // [pairs][2 slots][2 CTAs][kSub kPfTok tokens][128 rows]
+    uint32_t *cnt; // [pairs][2 CTAs][kGroups], by a split tile's first pair
 };
 
 template <int BITS>
 constexpr size_t pf_smem_bytes()
 {
     using C = PfCfg<BITS>;
-    return 1024 + (size_t)kPfXS * kPfXB + (size_t)C::kWS * C::kWB + 4 * kPfOutB + (size_t)kPfSS * 256 +
-           (size_t)C::kWS * 128 +
-           (size_t)(2 * kPfXS + 2 * C::kWS + 2 * kPfSS + 4) * 8 + 16;
+    return 1024 + (size_t)C::kXS * C::kXB + (size_t)C::kWS * C::kWB + 2 * C::kGroups * kPfOutB + (size_t)kPfSS * 256 +
+           (size_t)C::kWS * 128 + (size_t)(2 * C::kXS + 2 * C::kWS + 2 * kPfSS + C::kAS + 4) * 8 + 32;
 }
 
 // ---- pairs of CTAs ----
@@ -113,8 +129,7 @@ __device__ __forceinline__ void pf_arrive(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// Barrier of the four warps of one half of the retire warps, and whether all of
-// them are well.
+// Barrier of the four warps of a retire group, and whether all of them are well.
 __device__ __forceinline__ bool pf_all(int id, bool ok)
 {
     uint32_t r;
@@ -172,14 +187,12 @@ __device__ __forceinline__ void pf_commit(uint64_t *bar)
                  : "memory");
 }
 
-__device__ __forceinline__ void pf_ffma2(float &d0, float &d1, float a, float b0, float b1)
+// d += {a, a} {b0, b1}, a pair of fp32 sums kept packed (each half rounded as fmaf).
+__device__ __forceinline__ void pf_ffma2(unsigned long long &d, unsigned long long aa, float b0, float b1)
 {
-    unsigned long long d, aa, bb;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(d0), "f"(d1));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a));
+    unsigned long long bb;
     asm("mov.b64 %0, {%1, %2};" : "=l"(bb) : "f"(b0), "f"(b1));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(aa), "l"(bb));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
 }
 
 // Two int8 codes (bytes lo, lo + 1 of w) as exact bf16: with the low seven
@@ -215,16 +228,16 @@ __device__ __forceinline__ int pf_owner(const PfParams &p, int G, int u)
 
 // What a retire warp needs to write a tile out.
 struct PfRetire {
-    int ch0, nc; // the warp's half: first 16-token chunk of a tile, chunks
+    int ch0, nc; // the warp's group: first 16-token chunk of an accumulator, chunks
     int G, pair, rank, u0, u1;
-    float *obuf;      // the half's two output buffers
-    uint32_t *ticket; // the half's shared word
+    float *obuf;      // the group's two output buffers
+    uint32_t *ticket; // the group's shared word
     uint32_t ebar;    // the leader's accempty barriers
     uint32_t tq;      // the warp's corner of accumulator 0
 };
 
 // The output path: 16 tokens (a chunk) of the CTA's 128 channels at a time.  The
-// half's four warps put their sums into shared memory, a channel a thread, and
+// group's four warps put their sums into shared memory, a channel a thread, and
 // take them out as 8 consecutive channels of a token a thread, so that y and
 // the operands move in 16-byte pieces, 256 contiguous bytes a token.  (Written
 // 2 bytes a lane, 64 a warp, a tile with a residual took 38 us to leave.)
@@ -240,15 +253,20 @@ struct PfOut {
         const int t128 = threadIdx.x & 127;
         og = 8 * (t128 & 15);
         ot = t128 >> 4;
-        r = t128; // warps 4-7 and 8-11: lane quadrant warp % 4
+        r = t128; // the retire warps start at warp 4: lane quadrant warp % 4
         id = 1 + ((threadIdx.x - 128) >> 7);
-        ob = 0; // the half has met since the buffers were last read
+        ob = 0; // the group has met since the buffers were last read
         nn0 = (2 * (tile / p.TT) + rt.rank) * kPanelRows;
         vec_mul = ((reinterpret_cast<uintptr_t>(p.epi.mul) | (uintptr_t)(2 * p.epi.ld_mul)) & 15) == 0;
         vec_res = ((reinterpret_cast<uintptr_t>(p.epi.res) | (uintptr_t)(2 * p.epi.ld_res)) & 15) == 0;
     }
 
-    __device__ __forceinline__ int token(int c) const { return (tile % p.TT) * p.n + 16 * (rt.ch0 + c) + ot; }
+    // This thread's first token of chunk i (rt.nc chunks of each accumulator in turn).
+    __device__ __forceinline__ int token(int i) const
+    {
+        const int sub = i >= rt.nc ? 1 : 0;
+        return ((tile % p.TT) * p.nsub + sub) * p.n + 16 * (rt.ch0 + i - sub * rt.nc) + ot;
+    }
 
     static __device__ __forceinline__ uint4 row8(const uint16_t *src, bool vec)
     {
@@ -265,7 +283,7 @@ struct PfOut {
     __device__ __forceinline__ void fetch(int c)
     {
         const int nn = nn0 + og, m0 = token(c);
-        if (nn >= p.N || c >= rt.nc)
+        if (nn >= p.N || c >= rt.nc * p.nsub)
             return;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -335,32 +353,36 @@ struct PfOut {
     }
 };
 
-// A tile's sums stand in accumulator b: to y, or, for a tile that other pairs
-// share, to this pair's partial and, by the last of them to come (a ticket for
-// each CTA's half), added in the pairs' order to y.  The accumulator is released
-// after its last column is read.  Called by the four warps of a half together.
-// Out of line, so that the retire loop keeps its registers.
+// A tile's sums stand in accumulator b (INT8: in 0 and 1): to y, or, for a tile
+// that other pairs share, to this pair's partial and, by the last of them to
+// come (a ticket for each CTA's group), added in the pairs' order to y.  The
+// accumulators are released after the last column is read.  Called by the four
+// warps of a group together.  Out of line, so that the retire loop keeps its
+// registers.
 template <int BITS>
 __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int tile, int b)
 {
-    const int KB = p.KB, lane = threadIdx.x & 31;
+    constexpr int SUB = PfCfg<BITS>::kSub;
+    const int KB = p.KB, lane = threadIdx.x & 31, chunks = rt.nc * p.nsub;
     const bool whole = rt.u0 <= tile * KB && rt.u1 >= (tile + 1) * KB;
     PfOut out(p, rt, tile);
     float scale = 1.f;
     if (BITS == 8 && out.nn0 + out.r < p.N)
         scale = bf16_bits_to_float(p.scales[out.nn0 + out.r]);
-    auto part_of = [&](int c) { // pair c's partial of this tile
-        const int slot = pf_start(p, rt.G, c) / KB == tile ? 0 : 1;
-        return p.part + ((size_t)((c * 2 + slot) * 2 + rt.rank) * kPfTok + 16 * rt.ch0) * kPanelRows + out.r;
+    // pair c's partial of chunk i of this tile
+    auto part_of = [&](int c, int i) {
+        const int slot = pf_start(p, rt.G, c) / KB == tile ? 0 : 1, sub = i >= rt.nc ? 1 : 0;
+        return p.part + (((size_t)((c * 2 + slot) * 2 + rt.rank) * SUB + sub) * kPfTok +
+                         16 * (rt.ch0 + i - sub * rt.nc)) * kPanelRows + out.r;
     };
-    float *mine = part_of(rt.pair);
     if (whole)
         out.fetch(0);
-    for (int c = 0; c < rt.nc; ++c) {
+    for (int i = 0; i < chunks; ++i) {
         float v[16];
-        tmem_ld_32x32b_x16(rt.tq + b * kPfTok + 16 * c, v);
+        const int sub = i >= rt.nc ? 1 : 0;
+        tmem_ld_32x32b_x16(rt.tq + (b + sub) * kPfTok + 16 * (i - sub * rt.nc), v);
         tmem_wait_ld();
-        if (c == rt.nc - 1) {
+        if (i == chunks - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -371,14 +393,15 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     v[j] *= scale;
-            out.emit(c, v);
+            out.emit(i, v);
         } else {
+            float *mine = part_of(rt.pair, i);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                mine[(size_t)(16 * c + j) * kPanelRows] = v[j];
+                mine[j * kPanelRows] = v[j];
         }
     }
-    if (rt.nc == 0) { // a tile of 16 tokens: the other half has them
+    if (chunks == 0) { // few tokens: another group has them
         __syncwarp();
         if (lane == 0)
             pf_arrive(rt.ebar + b * 8);
@@ -386,7 +409,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
     if (whole)
         return;
     const int cf = pf_owner(p, rt.G, tile * KB), cl = pf_owner(p, rt.G, (tile + 1) * KB - 1);
-    uint32_t *counter = p.cnt + cf * 4 + rt.rank * 2 + out.id - 1;
+    uint32_t *counter = p.cnt + (cf * 2 + rt.rank) * PfCfg<BITS>::kGroups + out.id - 1;
     __threadfence();
     named_barrier_sync(out.id, 128);
     if (out.r == 0)
@@ -398,7 +421,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
         return;
     __threadfence();
     out.fetch(0);
-    for (int c = 0; c < rt.nc; ++c) {
+    for (int i = 0; i < chunks; ++i) {
         float t[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -408,7 +431,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (cc + e <= cl) {
-                    const float *src = part_of(cc + e) + (size_t)c * 16 * kPanelRows;
+                    const float *src = part_of(cc + e, i);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         v[e][j] = __ldcg(src + j * kPanelRows);
@@ -424,32 +447,33 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 t[j] *= scale;
-        out.emit(c, t);
+        out.emit(i, t);
     }
     if (out.r == 0)
         atomicExch(counter, 0u); // ready for the next call
 }
 
 template <int BITS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThreads, 1)
     gemm_pf_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ PfParams p)
 {
     using C = PfCfg<BITS>;
-    constexpr int WS = C::kWS, WB = C::kWB;
+    constexpr int WS = C::kWS, WB = C::kWB, XS = C::kXS, XB = C::kXB, UN = C::kUnroll;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sX = smem;                // kPfXS x stages, 1024-byte aligned
-    uint8_t *sW = sX + kPfXS * kPfXB;  // WS packed blocks
-    uint8_t *sO = sW + (size_t)WS * WB; // two output buffers for each half of the retire warps
-    uint8_t *sS = sO + 4 * kPfOutB;     // kPfSS group scales
+    uint8_t *sX = smem;                 // XS x stages, 1024-byte aligned
+    uint8_t *sW = sX + XS * XB;         // WS packed blocks
+    uint8_t *sO = sW + (size_t)WS * WB;           // two output buffers for each retire group
+    uint8_t *sS = sO + 2 * C::kGroups * kPfOutB; // kPfSS group scales
     uint8_t *sZ = sS + kPfSS * 256;    // WS zero points
-    uint64_t *full = reinterpret_cast<uint64_t *>(sZ + WS * 128);
-    uint64_t *done = full + kPfXS;
-    uint64_t *wfull = done + kPfXS, *wempty = wfull + WS;
+    uint64_t *xfull = reinterpret_cast<uint64_t *>(sZ + WS * 128);
+    uint64_t *done = xfull + XS;
+    uint64_t *afull = done + XS;
+    uint64_t *wfull = afull + C::kAS, *wempty = wfull + WS;
     uint64_t *sfull = wempty + WS, *sempty = sfull + kPfSS;
     uint64_t *accfull = sempty + kPfSS, *accempty = accfull + 2;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(accempty + 2);
-    uint32_t *s_ticket = s_tmem + 1; // [2 halves]
+    uint32_t *s_ticket = s_tmem + 1; // [kGroups]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = pf_rank();
@@ -459,8 +483,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     const int tile0 = u0 / KB, kb0 = u0 % KB;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPfXS; ++s) {
-            mbar_init(&full[s], 17); // the dequantization warps of both CTAs and the leader's expect_tx
+        for (int s = 0; s < XS; ++s) {
+            mbar_init(&xfull[s], 1); // the leader's expect_tx
             mbar_init(&done[s], 1);
         }
         for (int s = 0; s < WS; ++s) {
@@ -469,11 +493,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         }
         for (int s = 0; s < kPfSS; ++s) {
             mbar_init(&sfull[s], 1);
-            mbar_init(&sempty[s], 8);
+            mbar_init(&sempty[s], 4 * C::kGroups);
         }
+        for (int s = 0; s < C::kAS; ++s)
+            mbar_init(&afull[s], 16); // the dequantization warps of both CTAs
         for (int s = 0; s < 2; ++s) {
             mbar_init(&accfull[s], 1);
-            mbar_init(&accempty[s], 16); // the retire warps of both CTAs
+            mbar_init(&accempty[s], 2 * 4 * C::kGroups); // the retire warps of both CTAs
         }
         fence_mbar_init();
     }
@@ -490,28 +516,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     bool ok = true;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfRegsIssue));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsIssue));
         if (warp == 0 && lane == 0) {
             // ---------------- x producer ----------------
             pdl_wait(); // x may be written by the preceding kernel
             const uint64_t pol = policy_evict_last();
-            const int half = p.n >> 1, tx = p.n * 128; // both CTAs' bytes
-            const uint32_t bar = pf_map(full, 0);
-            int kb = kb0, tt = tile0 % p.TT, c1 = tt * p.n + (int)rank * half;
+            const int half = p.n >> 1, tx = p.nsub * p.n * 128; // tx: both CTAs' bytes
+            const uint32_t bar = pf_map(xfull, 0);
+            int kb = kb0, tt = tile0 % p.TT;
             for (int i = 0; i < 2 * nu; ++i) {
-                const int xs = i % kPfXS;
-                if (i >= kPfXS && !mbar_wait(&done[xs], ((i / kPfXS) - 1) & 1)) {
+                const int xs = i % XS;
+                if (i >= XS && !mbar_wait(&done[xs], ((i / XS) - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 if (rank == 0)
-                    mbar_arrive_expect_tx(&full[xs], tx);
-                pf_load_x(sX + xs * kPfXB, &tmx, kb * kBlockK + (i & 1) * 64, c1, bar + xs * 8, pol);
+                    mbar_arrive_expect_tx(&xfull[xs], tx);
+                for (int sub = 0; sub < p.nsub; ++sub)
+                    pf_load_x(sX + xs * XB + sub * kPfXB, &tmx, kb * kBlockK + (i & 1) * 64,
+                              (tt * p.nsub + sub) * p.n + (int)rank * half, bar + xs * 8, pol);
                 if ((i & 1) && ++kb == KB) {
                     kb = 0;
                     if (++tt == p.TT)
                         tt = 0;
-                    c1 = tt * p.n + (int)rank * half;
                 }
             }
         } else if (warp == 1 && lane == 0) {
@@ -568,61 +595,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             const bool issuer = pf_elect();
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.n >> 3) << 17) | (16u << 24);
             const uint64_t bdesc0 = smem_desc_sw128(smem_u32(sX));
-            const int steps = 2 * nu;
-            int kb = kb0, acc = 0; // acc: tiles begun (INT8)
-            uint32_t par = 0;
-            for (int i0 = 0; i0 < steps && ok; i0 += kPfXS, par ^= 1) {
+            int kb = kb0, tiles = 0; // tiles begun (INT8)
+            uint32_t par = 0;        // of this round of the x ring
+            for (int i0 = 0; i0 < nu && ok; i0 += UN, par ^= 1) {
 #pragma unroll
-                for (int j = 0; j < kPfXS; ++j) {
-                    if (i0 + j >= steps)
+                for (int uu = 0; uu < UN; ++uu) {
+                    if (i0 + uu >= nu)
                         break;
-                    bool fresh = (j & 1) == 0;
-                    int b = (j >> 1) & 1;
+                    const int as = uu & 1; // INT8: A stage; INT4: accumulator
+                    bool fresh = true;
                     if constexpr (BITS == 8) {
-                        fresh = fresh && (kb == 0 || i0 + j == 0);
-                        acc += fresh;
-                        b = (acc - 1) & 1;
+                        fresh = kb == 0 || i0 + uu == 0;
+                        // the last tile's sums must have been read
+                        if (fresh && ++tiles > 1)
+                            ok = ok && mbar_wait(&accempty[0], tiles & 1);
+                        ok = ok && mbar_wait(&afull[as], par);
+                    } else { // group g = i0 + uu waits for the release of g - 2
+                        if (i0 > 0 || uu >= 2)
+                            ok = ok && mbar_wait(&accempty[as], ((uu >> 1) + 1) & 1);
                     }
-                    if (fresh) { // the accumulator's last use must have been read
-                        bool free = true;
-                        if constexpr (BITS == 4) // group g = (i0 + j) / 2 waits for the release of g - 2
-                            free = (i0 == 0 && j < 4) || mbar_wait(&accempty[b], ((j >> 2) + 1) & 1);
-                        else
-                            free = acc <= 2 || mbar_wait(&accempty[b], ((acc - 3) >> 1) & 1);
-                        ok = ok && free;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int j = 2 * uu + hf;
+                        if constexpr (BITS == 4) // step 8 (round) + j: the stage's use j / 4 of the round's two
+                            ok = ok && mbar_wait(&afull[j % 4], (j >> 2) & 1);
+                        ok = ok && mbar_wait(&xfull[j], par);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        if (issuer) {
+                            const uint64_t bdesc = bdesc0 + (uint64_t)(j * (XB >> 4));
+                            const uint32_t d = tmem + (BITS == 4 ? as * kPfTok : 0);
+                            const uint32_t a = tmem + kPfA0 + (j % 4) * 32;
+                            const uint32_t keep = fresh && hf == 0 ? 0u : 1u;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                pf_mma(d, a + kk * 8, bdesc + (uint64_t)(kk * 2), idesc, kk == 0 ? keep : 1u);
+                            if (BITS == 8 && p.nsub == 2)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    pf_mma(d + kPfTok, a + kk * 8, bdesc + (uint64_t)((kPfXB >> 4) + kk * 2), idesc,
+                                           kk == 0 ? keep : 1u);
+                            pf_commit(&done[j]);
+                        }
+                        __syncwarp();
                     }
-                    ok = ok && mbar_wait(&full[j], par);
-                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
                         break;
-                    tc_fence_after();
-                    if (issuer) {
-                        const uint64_t bdesc = bdesc0 + (uint64_t)(j * (kPfXB >> 4));
-                        const uint32_t d = tmem + b * kPfTok, a = tmem + kPfA0 + (j % kPfAS) * 32;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            pf_mma(d, a + kk * 8, bdesc + (uint64_t)(kk * 2), idesc, (fresh && kk == 0) ? 0u : 1u);
-                        pf_commit(&done[j]);
-                    }
-                    if (j & 1) {
-                        if (++kb == KB)
-                            kb = 0;
-                        if (BITS == 8 && (kb == 0 || i0 + j == steps - 1) && issuer)
-                            pf_commit(&accfull[b]);
-                    }
+                    if (++kb == KB)
+                        kb = 0;
+                    if (BITS == 8 && (kb == 0 || i0 + uu == nu - 1) && issuer)
+                        pf_commit(&accfull[0]);
                     __syncwarp();
                 }
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 4 + 4 * C::kGroups) {
         // ---------------- retire warps ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfRegsRetire));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsRetire));
         pdl_wait(); // y and the workspace may still be in use by the preceding kernel
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int nch = p.n / 16;
+        static_assert(C::kGroups * C::kChunks * 16 == kPfTok, "the groups cover an accumulator");
         PfRetire rt;
-        rt.ch0 = h == 0 ? 0 : (nch + 1) / 2; // this warp's 16-column chunks
-        rt.nc = h == 0 ? (nch + 1) / 2 : nch - (nch + 1) / 2;
+        rt.ch0 = nch * h / C::kGroups; // this warp's 16-column chunks
+        rt.nc = nch * (h + 1) / C::kGroups - rt.ch0;
         rt.G = G;
         rt.pair = pair;
         rt.rank = (int)rank;
@@ -636,30 +674,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         const uint32_t tq = rt.tq;
 
         if constexpr (BITS == 4) {
-            float tot[kPfChunks * 16];
+            unsigned long long tot[C::kChunks * 8]; // pairs of fp32 sums
 #pragma unroll
-            for (int j = 0; j < kPfChunks * 16; ++j)
-                tot[j] = 0.f;
+            for (int j = 0; j < C::kChunks * 8; ++j)
+                tot[j] = 0ull;
             int tile = tile0, kb = kb0;
             for (int g = 0; g < nu; ++g) {
                 const int st = 2 * g + 1, ss = g % kPfSS; // the group's last step
                 // A warp whose wait gave up goes on without waiting, so that every
-                // warp of the half comes to the barriers of every tile.
-                ok = ok && mbar_wait_warp(&done[st % kPfXS], (st / kPfXS) & 1) &&
+                // warp of the group comes to the barriers of every tile.
+                ok = ok && mbar_wait_warp(&done[st % XS], (st / XS) & 1) &&
                      mbar_wait_warp(&sfull[ss], (g / kPfSS) & 1);
                 tc_fence_after();
                 const float s = bf16_bits_to_float(reinterpret_cast<const uint16_t *>(sS + ss * 256)[r]);
+                unsigned long long s2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
                 const uint32_t ta = tq + (g & 1) * kPfTok;
 #pragma unroll
-                for (int c = 0; c < kPfChunks; ++c) // 16 columns at a time: 32 would spill
-                    if (c < nc) {
-                        float v[16];
-                        tmem_ld_32x32b_x16(ta + 16 * c, v);
-                        tmem_wait_ld();
+                for (int c = 0; c < C::kChunks; c += 2) { // two loads in flight; columns past the group's are not used
+                    float v[2][16];
+                    tmem_ld_32x32b_x16(ta + 16 * c, v[0]);
+                    tmem_ld_32x32b_x16(ta + 16 * c + 16, v[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int j = 0; j < 16; j += 2)
-                            pf_ffma2(tot[16 * c + j], tot[16 * c + j + 1], s, v[j], v[j + 1]);
-                    }
+                            pf_ffma2(tot[8 * (c + e) + j / 2], s2, v[e][j], v[e][j + 1]);
+                }
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&sempty[ss]);
@@ -674,12 +716,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 // the tile's (or the run's) last group: the totals take its
                 // accumulator's place, so that writing them out needs few registers
 #pragma unroll
-                for (int c = 0; c < kPfChunks; ++c)
+                for (int c = 0; c < C::kChunks; ++c)
                     if (c < nc) {
                         uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            w[j] = __float_as_uint(tot[16 * c + j]);
+                        for (int j = 0; j < 8; ++j) {
+                            w[2 * j] = (uint32_t)tot[8 * c + j];
+                            w[2 * j + 1] = (uint32_t)(tot[8 * c + j] >> 32);
+                        }
                         tmem_st_32x32b_x16(ta + 16 * c, w);
                     }
                 tmem_wait_st();
@@ -687,47 +731,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 if (ok)
                     pf_flush<BITS>(p, rt, tile, g & 1);
 #pragma unroll
-                for (int j = 0; j < kPfChunks * 16; ++j)
-                    tot[j] = 0.f;
+                for (int j = 0; j < C::kChunks * 8; ++j)
+                    tot[j] = 0ull;
                 kb = 0;
                 ++tile;
             }
         } else {
             const int tile1 = nu > 0 ? (u1 - 1) / KB : tile0 - 1;
             for (int tile = tile0; tile <= tile1; ++tile) {
-                const int t = tile - tile0, b = t & 1;
-                ok = pf_all(1 + h, ok && mbar_wait_warp(&accfull[b], (t >> 1) & 1));
+                ok = pf_all(1 + h, ok && mbar_wait_warp(&accfull[0], (tile - tile0) & 1));
                 if (!ok)
-                    break; // the whole half
+                    break; // the whole group
                 tc_fence_after();
-                pf_flush<BITS>(p, rt, tile, b);
+                pf_flush<BITS>(p, rt, tile, 0);
             }
         }
     } else {
         // ---------------- dequantization warps ----------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfRegsDequant));
-        const int q = warp & 3, e = (warp - 12) >> 2;
-        const uint32_t bar = pf_map(full, 0);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsDequant));
+        const int q = warp & 3, e = (warp - 4 - 4 * C::kGroups) >> 2;
+        const uint32_t bar = pf_map(afull, 0);
         const int r = 32 * q + lane, g = lane >> 2, blkrow = 2 * q + e; // INT8: this lane's row; INT4: 16-row block
-        const int steps = 2 * nu;
-        // this lane's packed values of a step (the next step's are fetched while
-        // this one is converted and stored)
-        uint4 w[2];
+        constexpr int AH = C::kAH, V = BITS == 4 ? 1 : 2; // V: 16-byte pieces of 64 k
+        uint4 w[AH * V];                                  // this lane's packed values of an A stage
+        uint32_t zlo = 0, zhi = 0;
         int ws = 0;
         uint32_t wpar = 0;
-        auto fetch = [&](int hf) {
+        auto fetch = [&](int h0) { // halves h0 .. h0 + AH - 1 of weight stage ws
             const uint8_t *blk = sW + (size_t)ws * WB;
-            if constexpr (BITS == 4) {
-                w[0] = *reinterpret_cast<const uint4 *>(blk + blkrow * 1024 + hf * 512 + lane * 16);
-            } else {
-                const int c = 4 * hf + 2 * e; // two 16-k chunks of one row
-                w[0] = *reinterpret_cast<const uint4 *>(blk + int8_chunk_in_block(r, c));
-                w[1] = *reinterpret_cast<const uint4 *>(blk + int8_chunk_in_block(r, c + 1));
+#pragma unroll
+            for (int hf = 0; hf < AH; ++hf) {
+                if constexpr (BITS == 4) {
+                    w[hf] = *reinterpret_cast<const uint4 *>(blk + blkrow * 1024 + (h0 + hf) * 512 + lane * 16);
+                } else {
+                    const int c = 4 * (h0 + hf) + 2 * e; // two 16-k chunks of one row
+                    w[2 * hf] = *reinterpret_cast<const uint4 *>(blk + int8_chunk_in_block(r, c));
+                    w[2 * hf + 1] = *reinterpret_cast<const uint4 *>(blk + int8_chunk_in_block(r, c + 1));
+                }
             }
-        };
-        uint32_t zlo = 0, zhi = 0;
-        auto fetch_zeros = [&]() { // rows 16 blkrow + g and + 8
-            if constexpr (BITS == 4) {
+            if (BITS == 4 && h0 == 0) { // rows 16 blkrow + g and + 8
                 const uint8_t *zp = sZ + ws * 128 + 8 * blkrow + (g >> 1);
                 const uint32_t z0 = (zp[0] >> (4 * (g & 1))) & 0xFu, z1 = (zp[4] >> (4 * (g & 1))) & 0xFu;
                 zlo = 0x43004300u | z0 | (z0 << 16);
@@ -737,28 +779,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         ok = mbar_wait_warp(&wfull[0], 0);
         if (ok)
             fetch(0);
-        uint32_t par = 1; // of the steps four before, in the second half of each round
-        for (int i0 = 0; i0 < steps && ok; i0 += kPfXS, par ^= 1) {
+        // stages of a round of the x ring: INT4 eight of one half, INT8 two of two
+        constexpr int RS = XS / AH;
+        const int stages = 2 * nu / AH;
+        uint32_t par = 0; // of this round
+        for (int i0 = 0; i0 < stages && ok; i0 += RS, par ^= 1) {
 #pragma unroll
-            for (int j = 0; j < kPfXS; ++j) {
-                if (i0 + j >= steps)
+            for (int j = 0; j < RS; ++j) {
+                if (i0 + j >= stages)
                     break;
-                if ((j & 1) == 0)
-                    fetch_zeros();
-                uint32_t rr[16];
-                if constexpr (BITS == 4) {
-                    int4_tile_regs(w[0], zlo, zhi, rr);
-                } else {
-                    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+                uint32_t rr[AH][16];
 #pragma unroll
-                    for (int h = 0; h < 8; ++h) {
-                        rr[2 * h] = pf_s8pair(v[h], 0);
-                        rr[2 * h + 1] = pf_s8pair(v[h], 1);
+                for (int hf = 0; hf < AH; ++hf) {
+                    if constexpr (BITS == 4) {
+                        int4_tile_regs(w[hf], zlo, zhi, rr[hf]);
+                    } else {
+                        const uint4 a = w[2 * hf], b = w[2 * hf + 1];
+                        const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            rr[hf][2 * i] = pf_s8pair(v[i], 0);
+                            rr[hf][2 * i + 1] = pf_s8pair(v[i], 1);
+                        }
                     }
                 }
-                if ((j & 1) == 0) {
+                // the next stage's values, before this one's wait for its place
+                if (AH == 1 && (j & 1) == 0) {
                     fetch(1);
-                } else { // every value loaded from the stage has been used: release it, go to the next
+                } else { // every value loaded from the weight stage has been used: release it
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&wempty[ws]);
@@ -766,7 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         ws = 0;
                         wpar ^= 1;
                     }
-                    if (i0 + j + 1 < steps) {
+                    if (i0 + j + 1 < stages) {
                         if (!mbar_wait_warp(&wfull[ws], wpar)) {
                             ok = false;
                             break;
@@ -774,22 +822,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         fetch(0);
                     }
                 }
-                // the stage's last products: step i - 4, in slot (j + 4) % 8
-                if ((i0 > 0 || j >= kPfAS) && !mbar_wait_warp(&done[(j + kPfAS) % kPfXS], j < kPfAS ? par : par ^ 1)) {
+                // the A stage's last products: four halves back, in this round of
+                // the ring or (its first kAS stages) the last
+                const bool same = j >= C::kAS;
+                const int slot = ((j - C::kAS) * AH + AH - 1 + XS) % XS;
+                if ((i0 > 0 || same) && !mbar_wait_warp(&done[slot], same ? par : par ^ 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t ta = tmem + kPfA0 + (j % kPfAS) * 32;
-                if constexpr (BITS == 4)
-                    tmem_st_16x256b_x4(ta + ((uint32_t)(32 * q + 16 * e) << 16), rr);
-                else
-                    tmem_st_32x32b_x16(ta + ((uint32_t)(32 * q) << 16) + 16 * e, rr);
+                const uint32_t ta = tmem + kPfA0 + (j % C::kAS) * AH * 32 + ((uint32_t)(32 * q) << 16);
+#pragma unroll
+                for (int hf = 0; hf < AH; ++hf) {
+                    if constexpr (BITS == 4)
+                        tmem_st_16x256b_x4(ta + ((uint32_t)(16 * e) << 16) + 32 * hf, rr[hf]);
+                    else
+                        tmem_st_32x32b_x16(ta + 32 * hf + 16 * e, rr[hf]);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    pf_arrive(bar + j * 8);
+                    pf_arrive(bar + (j % C::kAS) * 8);
             }
         }
     }
@@ -837,7 +891,7 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
             return e;
         regs = fa.numRegs;
     }
-    if (regs * kPfThreads < 128 * kPfRegsIssue + 256 * kPfRegsRetire + 256 * kPfRegsDequant)
+    if (regs * PfCfg<BITS>::kThreads < PfCfg<BITS>::kRegs)
         return cudaErrorInvalidConfiguration;
     const Shape sh{a.bits, a.K, a.N, a.group};
     PfParams p;
@@ -845,9 +899,11 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
     p.N = a.N;
     p.KB = sh.kblocks();
     p.panels = sh.panels();
-    p.TT = (a.M + kPfTok - 1) / kPfTok;
-    p.n = ((a.M + p.TT - 1) / p.TT + 15) / 16 * 16;
-    p.TT = (a.M + p.n - 1) / p.n;
+    p.nsub = a.M <= kPfTok ? 1 : PfCfg<BITS>::kSub;
+    const int most_tok = p.nsub * kPfTok;
+    p.TT = (a.M + most_tok - 1) / most_tok;
+    p.n = ((a.M + p.TT * p.nsub - 1) / (p.TT * p.nsub) + 15) / 16 * 16;
+    p.TT = (a.M + p.nsub * p.n - 1) / (p.nsub * p.n);
     const long long tiles = (long long)((p.panels + 1) / 2) * p.TT, units = tiles * p.KB;
     if (units >= (1LL << 31))
         return cudaErrorInvalidValue; // the caller cuts M (pf_max_tokens)
@@ -860,12 +916,15 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
     p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.part = ws ? (float *)((uint8_t *)ws + ws_counter_bytes()) : nullptr;
-    p.align = ws ? 0 : 1;
     const int pairs = sm_count / 2 < kPfMaxPairs ? sm_count / 2 : kPfMaxPairs;
+    // Whole tiles a pair where the last round's idle pairs cost less than the
+    // split tiles' partial sums (about kPfSplitUnits units' time).
+    const long long rounds = (tiles + pairs - 1) / pairs;
+    p.align = !ws || rounds * p.KB <= units / pairs + kPfSplitUnits;
     // at least four units a pair: a tile's sums are not cut finer than 512 k
-    const long long want = ws ? (units + 3) / 4 : tiles;
-    const long long most = want > tiles ? want : tiles;
-    const int G = (int)(most < pairs ? most : pairs);
+    const long long want = p.align ? tiles : (units + 3) / 4;
+    const long long parts = want > tiles ? want : tiles;
+    const int G = (int)(parts < pairs ? parts : pairs);
     CUtensorMap map;
     if (!pf_x_map(&map, a.x, a.M, a.K, p.n / 2))
         return cudaErrorInvalidValue;
@@ -876,7 +935,7 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(2 * G);
-    cfg.blockDim = dim3(kPfThreads);
+    cfg.blockDim = dim3(PfCfg<BITS>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, gemm_pf_kernel<BITS>, map, p);
@@ -884,7 +943,7 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
 
 } // namespace
 
-size_t ws_bytes_gemm_pf() { return ws_counter_bytes() + (size_t)kPfMaxPairs * 4 * kPfTok * kPanelRows * sizeof(float); }
+size_t ws_bytes_gemm_pf() { return ws_counter_bytes() + (size_t)kPfMaxPairs * 4 * PfCfg<8>::kSub * kPfTok * kPanelRows * sizeof(float); }
 
 // Tokens of one launch: its units stay below 2^31.
 int pf_max_tokens(int K, int N)
