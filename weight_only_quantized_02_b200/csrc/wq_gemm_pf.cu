@@ -82,7 +82,7 @@ struct PfCfg {
     static constexpr int kThreads = 128 + kGroups * 128 + 256;
     // registers a thread at launch, and by role
     static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
-    static constexpr int kRegsIssue = 32, kRegsRetire = BITS == 4 ? 168 : 128,
+    static constexpr int kRegsIssue = 32, kRegsRetire = BITS == 4 ? 168 : 144,
                          kRegsDequant = BITS == 4 ? 56 : 80;
     static constexpr int kRegs = 128 * kRegsIssue + kGroups * 128 * kRegsRetire + 256 * kRegsDequant;
     static_assert(kRegs <= kThreads * kRegsLaunch, "the roles' registers come out of the CTA's at launch");
@@ -242,31 +242,41 @@ struct PfRetire {
 // the operands move in 16-byte pieces, 256 contiguous bytes a token.  (Written
 // 2 bytes a lane, 64 a warp, a tile with a residual took 38 us to leave.)
 struct PfOut {
-    const PfParams &p;
-    const PfRetire &rt;
-    int tile, nn0, og, ot, r, id, ob;
+    // copies: the launch parameters are behind a pointer here, and would be read
+    // again after every barrier
+    const int M, N, n, nc, act, out_f32;
+    const int tok0;         // this thread's first token of the tile, less 16 times the chunk
+    const int step1;        // from the first accumulator's last chunk to the second's first, less 16
+    const long long ld_mul, ld_res;
+    uint16_t *const y;
+    const uint16_t *const pmul, *const pres;
+    float *const obuf;
+    const int r, og, ot, id, nn; // channel written to shared memory; channels nn .. nn + 7 (og of the CTA's) and token taken out
+    int ob;
     bool vec_mul, vec_res;
     uint4 mul[2], res[2]; // the operands of this thread's two tokens of the next chunk
+    float bias[8];
 
-    __device__ __forceinline__ PfOut(const PfParams &p_, const PfRetire &rt_, int tile_) : p(p_), rt(rt_), tile(tile_)
+    // r: the retire warps start at warp 4, so a thread's place in its group is its
+    // lane quadrant's row
+    __device__ __forceinline__ PfOut(const PfParams &p, const PfRetire &rt, int tile)
+        : M(p.M), N(p.N), n(p.n), nc(rt.nc), act(p.epi.act), out_f32(p.epi.out_f32),
+          tok0((tile % p.TT) * p.nsub * p.n + 16 * rt.ch0 + ((int)(threadIdx.x & 127) >> 4)),
+          step1(p.n - 16 * rt.nc), ld_mul(p.epi.ld_mul), ld_res(p.epi.ld_res), y(p.y), pmul(p.epi.mul),
+          pres(p.epi.res), obuf(rt.obuf), r(threadIdx.x & 127), og(8 * (threadIdx.x & 15)),
+          ot((threadIdx.x & 127) >> 4), id(1 + ((threadIdx.x - 128) >> 7)),
+          nn((2 * (tile / p.TT) + rt.rank) * kPanelRows + 8 * (int)(threadIdx.x & 15))
     {
-        const int t128 = threadIdx.x & 127;
-        og = 8 * (t128 & 15);
-        ot = t128 >> 4;
-        r = t128; // the retire warps start at warp 4: lane quadrant warp % 4
-        id = 1 + ((threadIdx.x - 128) >> 7);
         ob = 0; // the group has met since the buffers were last read
-        nn0 = (2 * (tile / p.TT) + rt.rank) * kPanelRows;
-        vec_mul = ((reinterpret_cast<uintptr_t>(p.epi.mul) | (uintptr_t)(2 * p.epi.ld_mul)) & 15) == 0;
-        vec_res = ((reinterpret_cast<uintptr_t>(p.epi.res) | (uintptr_t)(2 * p.epi.ld_res)) & 15) == 0;
+        vec_mul = ((reinterpret_cast<uintptr_t>(pmul) | (uintptr_t)(2 * ld_mul)) & 15) == 0;
+        vec_res = ((reinterpret_cast<uintptr_t>(pres) | (uintptr_t)(2 * ld_res)) & 15) == 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            bias[j] = p.epi.bias && nn < N ? act16_to_float<false>(__ldg(p.epi.bias + nn + j)) : 0.f;
     }
 
-    // This thread's first token of chunk i (rt.nc chunks of each accumulator in turn).
-    __device__ __forceinline__ int token(int i) const
-    {
-        const int sub = i >= rt.nc ? 1 : 0;
-        return ((tile % p.TT) * p.nsub + sub) * p.n + 16 * (rt.ch0 + i - sub * rt.nc) + ot;
-    }
+    // This thread's first token of chunk i (nc chunks of each accumulator in turn).
+    __device__ __forceinline__ int token(int i) const { return tok0 + 16 * i + (i >= nc ? step1 : 0); }
 
     static __device__ __forceinline__ uint4 row8(const uint16_t *src, bool vec)
     {
@@ -279,68 +289,68 @@ struct PfOut {
         return make_uint4(v[0], v[1], v[2], v[3]);
     }
 
-    // Fetches the operands of chunk c.
-    __device__ __forceinline__ void fetch(int c)
+    // Fetches the operands of chunk i.
+    __device__ __forceinline__ void fetch(int i)
     {
-        const int nn = nn0 + og, m0 = token(c);
-        if (nn >= p.N || c >= rt.nc * p.nsub)
+        const int m0 = token(i);
+        if (nn >= N)
             return;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int m = m0 + 8 * e;
-            if (m < p.M && p.epi.mul)
-                mul[e] = row8(p.epi.mul + (long long)m * p.epi.ld_mul + nn, vec_mul);
-            if (m < p.M && p.epi.res)
-                res[e] = row8(p.epi.res + (long long)m * p.epi.ld_res + nn, vec_res);
+            if (m < M && pmul)
+                mul[e] = row8(pmul + (long long)m * ld_mul + nn, vec_mul);
+            if (m < M && pres)
+                res[e] = row8(pres + (long long)m * ld_res + nn, vec_res);
         }
     }
 
-    // Chunk c from this thread's 16 sums (channel r) to y, its operands fetched
-    // before; fetches the next chunk's.
-    __device__ __forceinline__ void emit(int c, const float (&v)[16])
+    // Chunk i from this thread's 16 sums (channel r) to y, its operands fetched
+    // before; fetches the next chunk's, if there is one.
+    __device__ __forceinline__ void emit(int i, bool next, const float (&v)[16])
     {
-        float *buf = rt.obuf + ob * (kPfOutB / 4);
+        float *buf = obuf + ob * (kPfOutB / 4);
         ob ^= 1; // a buffer is written again after the other one's barrier: its readers are through
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             buf[j * kPanelRows + r] = v[j];
         named_barrier_sync(id, 128);
         const uint4 cm[2] = {mul[0], mul[1]}, cr[2] = {res[0], res[1]};
-        fetch(c + 1);
-        const int nn = nn0 + og, m0 = token(c);
-        if (nn >= p.N)
+        if (next)
+            fetch(i + 1);
+        const int m0 = token(i);
+        if (nn >= N)
             return;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int m = m0 + 8 * e;
-            if (m >= p.M)
+            if (m >= M)
                 break;
             const float4 a = *reinterpret_cast<const float4 *>(buf + (ot + 8 * e) * kPanelRows + og);
             const float4 b = *reinterpret_cast<const float4 *>(buf + (ot + 8 * e) * kPanelRows + og + 4);
-            const size_t at = (size_t)m * p.N + nn;
-            if (p.epi.out_f32) {
-                float4 *yp = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.y) + at);
+            const size_t at = (size_t)m * N + nn;
+            if (out_f32) {
+                float4 *yp = reinterpret_cast<float4 *>(reinterpret_cast<float *>(y) + at);
                 yp[0] = a;
                 yp[1] = b;
                 continue;
             }
             float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            if (p.epi.bias)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] += act16_to_float<false>(__ldg(p.epi.bias + nn + j));
-            epi_activations(x, p.epi.act);
+            for (int j = 0; j < 8; ++j)
+                x[j] += bias[j];
+            epi_activations(x, act);
             const uint32_t mw[4] = {cm[e].x, cm[e].y, cm[e].z, cm[e].w};
             const uint32_t rw[4] = {cr[e].x, cr[e].y, cr[e].z, cr[e].w};
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 EpiOps lo{1.f, 0.f}, hi{1.f, 0.f};
-                if (p.epi.mul) {
+                if (pmul) {
                     lo.mul = __uint_as_float(mw[j] << 16);
                     hi.mul = __uint_as_float(mw[j] & 0xFFFF0000u);
                 }
-                if (p.epi.res) {
+                if (pres) {
                     lo.res = __uint_as_float(rw[j] << 16);
                     hi.res = __uint_as_float(rw[j] & 0xFFFF0000u);
                 }
@@ -348,7 +358,7 @@ struct PfOut {
                     __floats2bfloat162_rn(fmaf(x[2 * j], lo.mul, lo.res), fmaf(x[2 * j + 1], hi.mul, hi.res));
                 w[j] = *reinterpret_cast<const uint32_t *>(&q2);
             }
-            *reinterpret_cast<uint4 *>(p.y + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(y + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 };
@@ -363,12 +373,14 @@ template <int BITS>
 __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int tile, int b)
 {
     constexpr int SUB = PfCfg<BITS>::kSub;
-    const int KB = p.KB, lane = threadIdx.x & 31, chunks = rt.nc * p.nsub;
+    const int KB = p.KB, lane = threadIdx.x & 31, nc = rt.nc, chunks = nc * p.nsub;
+    const uint32_t tq = rt.tq + b * kPfTok;
     const bool whole = rt.u0 <= tile * KB && rt.u1 >= (tile + 1) * KB;
     PfOut out(p, rt, tile);
     float scale = 1.f;
-    if (BITS == 8 && out.nn0 + out.r < p.N)
-        scale = bf16_bits_to_float(p.scales[out.nn0 + out.r]);
+    const int row = out.nn - out.og + out.r; // the channel whose sums this thread holds
+    if (BITS == 8 && row < out.N)
+        scale = bf16_bits_to_float(p.scales[row]);
     // pair c's partial of chunk i of this tile
     auto part_of = [&](int c, int i) {
         const int slot = pf_start(p, rt.G, c) / KB == tile ? 0 : 1, sub = i >= rt.nc ? 1 : 0;
@@ -379,8 +391,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
         out.fetch(0);
     for (int i = 0; i < chunks; ++i) {
         float v[16];
-        const int sub = i >= rt.nc ? 1 : 0;
-        tmem_ld_32x32b_x16(rt.tq + (b + sub) * kPfTok + 16 * (i - sub * rt.nc), v);
+        tmem_ld_32x32b_x16(tq + 16 * i + (i >= nc ? kPfTok - 16 * nc : 0), v);
         tmem_wait_ld();
         if (i == chunks - 1) {
             tc_fence_before();
@@ -393,7 +404,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     v[j] *= scale;
-            out.emit(i, v);
+            out.emit(i, i + 1 < chunks, v);
         } else {
             float *mine = part_of(rt.pair, i);
 #pragma unroll
@@ -447,7 +458,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 t[j] *= scale;
-        out.emit(i, t);
+        out.emit(i, i + 1 < chunks, t);
     }
     if (out.r == 0)
         atomicExch(counter, 0u); // ready for the next call
