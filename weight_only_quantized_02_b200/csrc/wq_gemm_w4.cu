@@ -137,12 +137,16 @@ constexpr size_t gemm_w4_smem_bytes()
 // 128-byte row segment per warp; CG contributors x 16 tokens are in flight
 // together (this runs at the very end of the call, on its critical path).
 // Called after the retire loop, whose register totals are dead by then.
+// whole: this CTA (cf = cl) had the panel to itself and its totals stand in its
+// second slot.
 template <int NT, int CW, bool EPI>
 __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &sk, int pnl, int cf, int cl, int r,
-                                         int t0)
+                                         int t0, bool whole = false)
 {
     const int nrow = pnl * kPanelRows + r;
-    constexpr int CG = 4;
+    // fewer in flight beside an epilogue's operands from 64 tokens on, whose totals
+    // would spill otherwise (64 tokens: 50 us without any operand; the plain layer 33)
+    constexpr int CG = EPI && NT >= 64 ? 2 : 4, EB = NT >= 64 ? 8 : 16;
     for (int j0 = 0; j0 < CW; j0 += 16) {
         float acc[16];
 #pragma unroll
@@ -154,7 +158,7 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
             for (int u = 0; u < CG; ++u) {
                 const int cc = c0 + u;
                 if (cc <= cl) {
-                    const int sl = pnl == sk.first[cc] ? 0 : 1;
+                    const int sl = pnl == sk.first[cc] && !whole ? 0 : 1;
                     const float *src = p.part + ((size_t)(cc * 2 + sl) * NT + t0 + j0) * kPanelRows + r;
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -170,14 +174,14 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
         }
         if (nrow < p.N) {
             const int jn = min(16, p.M - t0 - j0);
-            epi_store_tokens<EPI, 16>(p.epi, p.y, p.N, t0 + j0, jn, nrow, acc);
+            epi_store_tokens<EPI, 16, EB>(p.epi, p.y, p.N, t0 + j0, jn, nrow, acc);
         }
     }
 }
 
 template <int NT, bool EPI>
 __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const __grid_constant__ CUtensorMap tmx,
-                                                                const GemmW4Params p)
+                                                                const __grid_constant__ GemmW4Params p)
 {
     using C = W4Cfg<NT>;
     constexpr int XS = C::kXS, SS = C::kSS, AS = C::kAS, ACC = C::kACC, DEPTH = C::kDepth, SLOT = C::kSlot;
@@ -328,9 +332,17 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const _
             const int nrow = pnl * kPanelRows + r;
             const int t0 = c * CW; // first token of this slice
             if (lo == pnl * KB && hi == (pnl + 1) * KB) {
-                if (nrow < p.N) {
+                if constexpr (EPI) {
+                    // through the second slot (the last panel's, not in use yet), so
+                    // that the totals need no registers while y is written
+                    float *mine = p.part + ((size_t)(cta * 2 + 1) * NT + t0) * kPanelRows + r;
+#pragma unroll
+                    for (int j = 0; j < CW; ++j)
+                        mine[j * kPanelRows] = tot[j];
+                    w4_fixup<NT, CW, true>(p, sk, pnl, cta, cta, r, t0, true); // each thread reads what it wrote
+                } else if (nrow < p.N) {
                     const int jn = min(CW, p.M - t0); // tokens of this slice that exist
-                    epi_store_tokens<EPI, CW>(p.epi, p.y, p.N, t0, jn, nrow, tot);
+                    epi_store_tokens<false, CW>(p.epi, p.y, p.N, t0, jn, nrow, tot);
                 }
                 return;
             }
