@@ -22,17 +22,19 @@
 // eight SMs.  A CTA reads its slice in batches of kUnroll 16-byte vectors per
 // thread, the next batch's loads in flight while it works on this one.
 //
-// Alternatives: a logit is a 64-bit key (value, then the complement of its
-// index), so all keys differ and the k largest are unique.  In the first batch
-// the largest key of every thread is known; a key that at least k of them
-// reach is found by a search over the keys with one block-wide count per
-// step, and only logits that reach it are kept (at most kUnroll vectors for
-// each thread counted, usually little more than k).  Later batches are only
-// compared with that bound, a vector at a time, and add the few that pass.
-// If a batch would overflow the list (rows that rise from end to end), the
-// list is cut back to its k best and the bound raised first.  At the end each
-// CTA sorts its best k by counting, and an entry's place in the row's answer
-// is its place in its own list plus the entries above it in the other CTAs'.
+// Alternatives: the loop over the logits does nothing for them.  Behind it every
+// thread knows the largest of the logits it read; a value that the maxima of at
+// least k threads reach (and of few more: a search with one block-wide count a
+// step) is reached by at least k logits, and only those threads' logits can be
+// among the k largest.  Their few vectors are read again, by all threads
+// together, out of L2, and what reaches the value is kept and ranked.  Where more
+// reaches it than the list holds (rows of few distinct values, masks) the k-th
+// largest value is found by counting over those vectors, everything above it
+// kept, and of the logits equal to it the first in the row, by a scan that ends
+// with them.  A logit is ranked by a 64-bit key (value, then the complement of
+// its index), so all keys differ and the answer is unique.
+// (Collecting during the loop, against a bound raised as it went, took 307 us
+// for 2048 rows of 152064 logits and k = 5, against 127 without alternatives.)
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
@@ -48,9 +50,11 @@ namespace wq {
 
 namespace {
 
-constexpr int kUnroll = 4;        // 16-byte vectors per thread and batch
-constexpr int kSortMax = 192;     // candidates ranked by counting without a cut first
+constexpr int kUnroll = 4;     // 16-byte vectors per thread and batch
+constexpr int kSortMax = 192;  // candidates ranked by counting without a cut first
+constexpr int kListMax = 1024; // candidates of a CTA
 constexpr int kLpMaxCluster = 8;
+constexpr int kShortBatches = 4; // rows of at most this many batches of a 128-thread CTA go to one
 
 typedef unsigned long long key_t64;
 
@@ -63,13 +67,9 @@ struct LpParams {
     int32_t *top_idx;
 };
 
-// The list must take what one bounded batch can add to k kept entries.
-__host__ __device__ constexpr int lp_accept(int k) { return k + k / 2 + 8; } // threads a bound may let through
-template <int VE>
-__host__ __device__ constexpr int lp_cap(int k)
-{
-    return lp_accept(k) * kUnroll * VE + k + 2 * VE; // + the elements outside the aligned vectors
-}
+// Threads (or candidates) that a bound for k may let through where it can.
+__host__ __device__ constexpr int lp_accept(int k) { return k + k / 2 + 8; }
+static_assert(lp_accept(kTopkMaxK) <= kSortMax, "a cut list can be ranked");
 
 template <class T>
 struct LpType;
@@ -151,12 +151,10 @@ __device__ __forceinline__ float value32(uint32_t o)
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
-// Every key is above 0, which stands for "none" (order32 > 0: the smallest, of
-// -inf, is 0x007FFFFF).
-__device__ __forceinline__ key_t64 make_key(float f, int idx)
-{
-    return ((key_t64)order32(f) << 32) | (uint32_t)~idx;
-}
+// A candidate's key: order32, then the complement of its index.  Every key is
+// above 0, which stands for "none" (the smallest order32, of -inf, is 0x007FFFFF).
+constexpr uint32_t kOrderInf = 0xFF800000u; // order32(+inf)
+constexpr uint32_t kOrderNan = 0xFFFFFFFFu;
 
 // ---------------------------------------------------------------------------
 // Running softmax sums
@@ -248,48 +246,55 @@ __device__ __forceinline__ key_t64 cluster_ld_u64(uint32_t a)
 // Selection
 // ---------------------------------------------------------------------------
 
-// A bound that between k and lp_accept(k) of the threads' keys reach, or 0
-// if fewer than k threads have one.  The keys differ, so the search ends: its
-// interval halves, and a bound with exactly k above it exists.  Called by the
-// whole CTA.
-__device__ __forceinline__ key_t64 bound_of_threads(key_t64 mine, int k)
+// A value that at least k of the threads' keys reach, and at most lp_accept(k)
+// of them unless too many are equal to the k-th largest; 0 if fewer than k
+// threads have a key.  top: no key is above it.  Called by the whole CTA.
+__device__ __forceinline__ uint32_t bound_of_threads(uint32_t mine, uint32_t top, int k)
 {
-    key_t64 lo = 0, hi = ~0ull; // at least k reach lo (0: everything); fewer than k reach hi
     if (__syncthreads_count(mine != 0) < k)
         return 0;
-    for (;;) {
-        const key_t64 mid = lo + (hi - lo) / 2;
-        if (mid == lo)
-            return lo;
+    uint32_t lo = 0, hi = top; // at least k reach lo; fewer than k are above hi
+    while (lo < hi) {
+        const uint32_t mid = hi - (hi - lo) / 2; // above lo
         const int c = __syncthreads_count(mine >= mid);
         if (c >= k && c <= lp_accept(k))
             return mid;
         if (c < k)
-            hi = mid;
+            hi = mid - 1;
         else
             lo = mid;
     }
+    return lo;
 }
 
-// The same over the n keys of a list, each thread counting its share.
+// The sum of c over the CTA, for everyone; slot alternates between calls.
+__device__ __forceinline__ int block_sum(int c, int *s_count, int &slot)
+{
+    if (threadIdx.x == 0)
+        s_count[slot] = 0;
+    __syncthreads();
+    c = __reduce_add_sync(0xffffffffu, c);
+    if ((threadIdx.x & 31) == 0 && c)
+        atomicAdd(&s_count[slot], c);
+    __syncthreads();
+    c = s_count[slot];
+    slot ^= 1; // the word just read is written again after the next call's barriers
+    return c;
+}
+
+// A bound that between k and lp_accept(k) of the n >= k different keys of a list
+// reach.
 __device__ __forceinline__ key_t64 bound_of_list(const key_t64 *list, int n, int k, int *s_count)
 {
-    key_t64 lo = 0, hi = ~0ull;
-    for (int slot = 0;; slot ^= 1) {
+    key_t64 lo = 0, hi = ~0ull; // at least k reach lo; fewer than k (or the accepted few) reach hi
+    for (int slot = 0;;) {
         const key_t64 mid = lo + (hi - lo) / 2;
         if (mid == lo)
             return lo;
-        if (threadIdx.x == 0)
-            s_count[slot] = 0;
-        __syncthreads();
         int c = 0;
         for (int i = threadIdx.x; i < n; i += blockDim.x)
             c += list[i] >= mid;
-        c = __reduce_add_sync(0xffffffffu, c);
-        if ((threadIdx.x & 31) == 0 && c)
-            atomicAdd(&s_count[slot], c);
-        __syncthreads();
-        c = s_count[slot];
+        c = block_sum(c, s_count, slot);
         if (c >= k && c <= lp_accept(k))
             return mid;
         if (c < k)
@@ -317,57 +322,215 @@ __device__ __forceinline__ void rank_into(const key_t64 *src, int n, int k, key_
     __syncthreads();
 }
 
+template <int THREADS>
 struct LpShared {
-    key_t64 cut[kSortMax];      // a list cut back before it is ranked
-    key_t64 best[kTopkMaxK];    // this CTA's k best, in order
+    key_t64 list[kListMax];  // candidates
+    key_t64 cut[kSortMax];   // a list cut back before it is ranked
+    key_t64 best[kTopkMaxK]; // this CTA's k best, in order
     key_t64 others[kLpMaxCluster * kTopkMaxK];
     Sums warp_sums[32];
     Sums sums; // this CTA's
-    int count; // entries of the list
-    int cut_count;
-    int list_count[2];
+    uint16_t chosen[THREADS]; // threads whose logits may be among the k largest
+    int chosen_count, count, cut_count, list_count[2];
+    int warp_count[32];
 };
 
 // The list's k best, in order, into sh.best.
-__device__ __forceinline__ void sort_list(LpShared &sh, const key_t64 *list, int n, int k)
+template <class Shared>
+__device__ __forceinline__ void sort_list(Shared &sh, int n, int k)
 {
     if (n <= kSortMax) {
-        rank_into(list, n, k, sh.best);
+        rank_into(sh.list, n, k, sh.best);
         return;
     }
-    const key_t64 b = bound_of_list(list, n, k, sh.list_count);
+    const key_t64 b = bound_of_list(sh.list, n, k, sh.list_count);
     if (threadIdx.x == 0)
         sh.cut_count = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x)
-        if (list[i] >= b)
-            sh.cut[atomicAdd(&sh.cut_count, 1)] = list[i]; // at most lp_accept(k) <= kSortMax
+        if (sh.list[i] >= b)
+            sh.cut[atomicAdd(&sh.cut_count, 1)] = sh.list[i]; // at most lp_accept(k) <= kSortMax
     __syncthreads();
     rank_into(sh.cut, sh.cut_count, k, sh.best);
 }
-static_assert(lp_accept(kTopkMaxK) <= kSortMax, "a cut list can be ranked");
+
+// A CTA's slice of a row: elements [e0, e1), of which [v0, v0 + nv VE) are whole
+// aligned vectors, vector i read by thread i mod THREADS, and the up to 2 VE - 2
+// others, before and behind them, by one thread each.
+template <class T, int THREADS>
+struct Slice {
+    static constexpr int VE = LpType<T>::VE;
+    const T *row;
+    int e0, e1, v0, nv;
+    __device__ __forceinline__ Slice(const T *row_, int e0_, int e1_) : row(row_), e0(e0_), e1(e1_)
+    {
+        const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(row + e0) & 15)) & 15) / (int)sizeof(T);
+        v0 = min(e1, e0 + lead);
+        nv = (e1 - v0) / VE;
+    }
+    __device__ __forceinline__ const uint4 *vec() const { return reinterpret_cast<const uint4 *>(row + v0); }
+    __device__ __forceinline__ int edge() const // this thread's element outside the vectors, or -1
+    {
+        const int t = threadIdx.x, n0 = v0 - e0, tail = v0 + nv * VE;
+        return t < n0 ? e0 + t : t < n0 + e1 - tail ? tail + t - n0 : -1;
+    }
+};
+
+// Elements of the vectors of the chosen threads and of the edges whose order32
+// is above o (at least o with or_equal): f(order32, index) for each, from any
+// thread.  The vectors come out of L2.
+template <class T, int THREADS, class Shared, class F>
+__device__ __forceinline__ void each_above(const Slice<T, THREADS> &sl, const Shared &sh, uint32_t o, bool or_equal, F f)
+{
+    using L = LpType<T>;
+    constexpr int VE = L::VE;
+    const int per = (sl.nv + THREADS - 1) / THREADS; // vectors of a thread, at most
+    const int items = sh.chosen_count * per;
+    for (int i = threadIdx.x; i < items; i += THREADS) {
+        const int v = (i % per) * THREADS + sh.chosen[i / per];
+        if (v >= sl.nv)
+            continue;
+        const uint4 q = __ldg(sl.vec() + v);
+#pragma unroll
+        for (int j = 0; j < VE / 2; ++j) {
+            const float2 x = L::pair(q, j);
+            const uint32_t a = order32(x.x), b = order32(x.y);
+            if (a > o || (or_equal && a == o))
+                f(a, sl.v0 + v * VE + 2 * j);
+            if (b > o || (or_equal && b == o))
+                f(b, sl.v0 + v * VE + 2 * j + 1);
+        }
+    }
+    const int e = sl.edge();
+    if (e >= 0) {
+        const uint32_t a = order32(to_float(sl.row[e]));
+        if (a > o || (or_equal && a == o))
+            f(a, e);
+    }
+}
+
+// Appends the first `want` elements equal to order32 o of the slice, in index
+// order, behind the `have` entries of the list.
+template <class T, int THREADS, class Shared>
+__device__ __noinline__ void first_equal(const Slice<T, THREADS> &sl, Shared &sh, uint32_t o, int have, int want)
+{
+    using L = LpType<T>;
+    constexpr int VE = L::VE;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n0 = sl.v0 - sl.e0, tail = sl.v0 + sl.nv * VE;
+    // rounds of up to VE consecutive elements a thread: the lead, THREADS vectors at a time, the tail
+    const int rounds = 2 + (sl.nv + THREADS - 1) / THREADS;
+    for (int r = 0; r < rounds && want > 0; ++r) {
+        uint32_t hit = 0; // bit j: element j of this thread's run equals o
+        int at = 0;
+        if (r == 0 || r == rounds - 1) {
+            at = r == 0 ? sl.e0 + (int)threadIdx.x : tail + (int)threadIdx.x;
+            if ((int)threadIdx.x < (r == 0 ? n0 : sl.e1 - tail))
+                hit = order32(to_float(sl.row[at])) == o;
+        } else {
+            const int v = (r - 1) * THREADS + (int)threadIdx.x;
+            at = sl.v0 + v * VE;
+            if (v < sl.nv) {
+                const uint4 q = __ldg(sl.vec() + v);
+#pragma unroll
+                for (int j = 0; j < VE / 2; ++j) {
+                    const float2 x = L::pair(q, j);
+                    hit |= (uint32_t)(order32(x.x) == o) << (2 * j) | (uint32_t)(order32(x.y) == o) << (2 * j + 1);
+                }
+            }
+        }
+        const int c = __popc(hit);
+        int inc = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d)
+                inc += u;
+        }
+        if (lane == 31)
+            sh.warp_count[warp] = inc;
+        __syncthreads();
+        int before = inc - c, total = 0;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            before += w < warp ? sh.warp_count[w] : 0;
+            total += sh.warp_count[w];
+        }
+        for (int j = 0; hit; ++j, hit >>= 1)
+            if ((hit & 1u) && before < want) {
+                sh.list[have + before] = ((key_t64)o << 32) | (uint32_t)~(at + j);
+                ++before;
+            }
+        __syncthreads(); // warp_count is written again
+        have += min(total, want);
+        want -= min(total, want);
+    }
+}
+
+// The slice's k best, in order, into sh.best.  mine: order32 that the largest
+// logit this thread read reaches, 0 if it read none; top: no logit is above it.
+template <class T, int THREADS, class Shared>
+__device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared &sh, uint32_t mine, uint32_t top, int k)
+{
+    if (threadIdx.x == 0)
+        sh.chosen_count = sh.count = 0;
+    const uint32_t bound = bound_of_threads(mine, min(top, kOrderInf), k); // has a barrier
+    if (mine != 0 && mine >= bound)
+        sh.chosen[atomicAdd(&sh.chosen_count, 1)] = (uint16_t)threadIdx.x;
+    __syncthreads();
+    each_above(sl, sh, bound, true, [&](uint32_t o, int idx) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kListMax)
+            sh.list[at] = ((key_t64)o << 32) | (uint32_t)~idx;
+    });
+    __syncthreads();
+    int n = sh.count;
+    if (n > kListMax) {
+        // the k-th largest value: the largest that at least k elements reach
+        uint32_t lo = bound, hi = top;
+        int slot = 0;
+        while (lo < hi) {
+            const uint32_t mid = hi - (hi - lo) / 2;
+            int c = 0;
+            each_above(sl, sh, mid, true, [&](uint32_t, int) { ++c; });
+            if (block_sum(c, sh.list_count, slot) >= k)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        __syncthreads(); // every thread has read sh.count
+        if (threadIdx.x == 0)
+            sh.count = 0;
+        __syncthreads();
+        each_above(sl, sh, lo, false, [&](uint32_t o, int idx) { // fewer than k
+            sh.list[atomicAdd(&sh.count, 1)] = ((key_t64)o << 32) | (uint32_t)~idx;
+        });
+        __syncthreads();
+        n = sh.count;
+        first_equal(sl, sh, lo, n, k - n);
+        __syncthreads();
+        n = k;
+    }
+    sort_list(sh, n, k);
+}
 
 template <class T, int THREADS, bool TOPK>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const LpParams p)
 {
     using L = LpType<T>;
     constexpr int VE = L::VE, B = THREADS * kUnroll; // vectors per batch
-    extern __shared__ key_t64 s_list[];              // lp_cap(k) candidates (TOPK)
-    __shared__ LpShared sh;
+    __shared__ LpShared<THREADS> sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = p.C > 1 ? (int)cluster_rank() : 0;
     const int m = blockIdx.x / p.C, k = p.k;
-    const int cap = lp_cap<VE>(k);
 
     pdl_launch_dependents();
     pdl_wait(); // the logits may come from the preceding kernel
 
     const T *row = static_cast<const T *>(p.logits) + (long long)m * p.ld;
-    const int e0 = min(p.N, rank * p.slice), e1 = min(p.N, e0 + p.slice);
-    // whole aligned vectors [v0, v0 + nv VE); the elements before and after them one by one
-    const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(row + e0) & 15)) & 15) / (int)sizeof(T);
-    const int v0 = min(e1, e0 + lead), nv = (e1 - v0) / VE;
-    const uint4 *vec = reinterpret_cast<const uint4 *>(row + v0);
+    const int e0 = min(p.N, rank * p.slice);
+    const Slice<T, THREADS> sl(row, e0, min(p.N, e0 + p.slice));
+    const int nv = sl.nv;
+    const uint4 *vec = sl.vec();
 
     int token = -1;
     float x_token = 0.f;
@@ -392,43 +555,25 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     load(0, cur);
 
     Sums a{-FLT_MAX, 0.f, 0.f};
-    key_t64 bound = 0;
-    float bound_f = -INFINITY; // the bound's value, once a batch has set it
-
-    // the up to 2 VE elements outside the aligned vectors: one thread each
-    const int tail0 = v0 + nv * VE;
-    const int edge = (int)threadIdx.x < v0 - e0            ? e0 + (int)threadIdx.x
-                     : (int)threadIdx.x < v0 - e0 + e1 - tail0 ? tail0 + (int)threadIdx.x - (v0 - e0)
-                                                               : -1;
-    float edge_x = 0.f;
+    float largest = -INFINITY; // a.m starts at the lowest finite value, above -inf
+    const int edge = sl.edge();
     if (edge >= 0) {
-        edge_x = to_float(row[edge]);
-        a.m = fmaxf(a.m, edge_x);
-        const float d = diff_clamped(edge_x, a.m);
+        const float x = to_float(row[edge]);
+        largest = x;
+        a.m = fmaxf(a.m, x);
+        const float d = diff_clamped(x, a.m);
         a.s = exp_nat(d);
         a.w = a.s * d;
     }
-    if constexpr (TOPK) {
-        if (threadIdx.x == 0)
-            sh.count = 0;
-        __syncthreads();
-        if (edge >= 0)
-            s_list[atomicAdd(&sh.count, 1)] = make_key(edge_x, edge);
-    }
 
-    for (int b = 0; b == 0 || b < nv; b += B) {
-        const bool more = b + B < nv;
-        if (more)
+    for (int b = 0; b < nv; b += B) {
+        if (b + B < nv)
             load(b + B, nxt);
-        // ---- running softmax sums ----
-        float vm[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            vm[u] = L::vmax(cur[u]);
-        float bm = vm[0];
+        float bm = L::vmax(cur[0]); // fmaxf below drops a NaN; the sums keep it
 #pragma unroll
         for (int u = 1; u < kUnroll; ++u)
-            bm = fmaxf(bm, vm[u]);
+            bm = fmaxf(bm, L::vmax(cur[u]));
+        largest = fmaxf(largest, bm);
         if (bm > a.m)
             rescale(a, bm);
         float2 s2 = make_float2(0.f, 0.f), w2 = s2;
@@ -447,83 +592,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         a.s += s2.x + s2.y;
         a.w += w2.x + w2.y;
 
-        // ---- candidates ----
-        if constexpr (TOPK) {
-            // the largest key of this thread's batch (bound 0: of everything there is)
-            auto largest = [&]() {
-                key_t64 best = 0;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int i = b + u * THREADS + (int)threadIdx.x;
-                    if (i < nv)
-#pragma unroll
-                        for (int j = 0; j < VE / 2; ++j) {
-                            const float2 f = L::pair(cur[u], j);
-                            const key_t64 k0 = make_key(f.x, v0 + i * VE + 2 * j), k1 = make_key(f.y, v0 + i * VE + 2 * j + 1);
-                            best = best > k0 ? best : k0;
-                            best = best > k1 ? best : k1;
-                        }
-                }
-                return best;
-            };
-            // appends the keys that reach the bound; an overfull list only counts on
-            auto append = [&]() {
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int i = b + u * THREADS + (int)threadIdx.x;
-                    if (i < nv && !(vm[u] < bound_f))
-#pragma unroll
-                        for (int j = 0; j < VE / 2; ++j) {
-                            const float2 f = L::pair(cur[u], j);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const key_t64 key = make_key(h ? f.y : f.x, v0 + i * VE + 2 * j + h);
-                                if (key >= bound) {
-                                    const int at = atomicAdd(&sh.count, 1);
-                                    if (at < cap)
-                                        s_list[at] = key;
-                                }
-                            }
-                        }
-                }
-            };
-            if (b == 0) {
-                bound = bound_of_threads(largest(), k);
-                bound_f = bound ? value32((uint32_t)(bound >> 32)) : -INFINITY;
-                append();
-            } else {
-                bool any = false;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
-                    any |= !(vm[u] < bound_f);
-                // the list's length before this batch, to go back to if it overflows
-                const bool some = __syncthreads_or(any);
-                if (some) {
-                    const int before = sh.count;
-                    __syncthreads();
-                    append();
-                    __syncthreads();
-                    if (sh.count > cap) { // keep the k best so far, raise the bound, take the batch again
-                        sort_list(sh, s_list, before, k);
-                        const key_t64 kth = sh.best[k - 1];
-                        bound = bound_of_threads(largest(), k);
-                        bound = bound > kth ? bound : kth;
-                        bound_f = bound ? value32((uint32_t)(bound >> 32)) : -INFINITY;
-                        const int keep = min(before, k);
-                        for (int i = threadIdx.x; i < keep; i += THREADS)
-                            s_list[i] = sh.best[i];
-                        if (threadIdx.x == 0)
-                            sh.count = keep;
-                        __syncthreads();
-                        append();
-                    }
-                }
-            }
-        }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             cur[u] = nxt[u];
     }
+
+    // order32 of this thread's largest, or, where a NaN sum tells of a NaN or +inf
+    // in it, what it reaches at least
+    uint32_t mine = 0;
+    if (edge >= 0 || (int)threadIdx.x < nv)
+        mine = a.s != a.s ? kOrderInf : order32(largest);
 
     // ---- the CTA's sums: lanes, then warps, in a fixed order ----
 #pragma unroll
@@ -544,7 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     for (int i = 1; i < THREADS / 32; ++i)
         merge(t, sh.warp_sums[i]);
     if constexpr (TOPK)
-        sort_list(sh, s_list, sh.count, k);
+        select_best(sl, sh, mine, t.s != t.s ? kOrderNan : order32(t.m), k);
     if (p.C > 1) {
         if (threadIdx.x == 0)
             sh.sums = t;
@@ -602,11 +680,6 @@ template <class T, int THREADS, bool TOPK>
 cudaError_t launch_lp(LpParams p, int sm_count, cudaStream_t st)
 {
     constexpr int VE = LpType<T>::VE;
-    const size_t smem = TOPK ? (size_t)lp_cap<VE>(p.k) * sizeof(key_t64) : 0;
-    const void *f = (const void *)logprobs_kernel<T, THREADS, TOPK>;
-    cudaError_t e = kernel_setup(f, smem, 0, 0, nullptr);
-    if (e != cudaSuccess)
-        return e;
     // CTAs of a row: while they fit the GPU at once with the others', and each
     // has a batch's work at least
     const long long slots = (long long)sm_count * (1024 / THREADS);
@@ -627,15 +700,23 @@ cudaError_t launch_lp(LpParams p, int sm_count, cudaStream_t st)
     cfg.numAttrs = C > 1 ? 2 : 1;
     cfg.gridDim = dim3((unsigned)p.M * C);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS, TOPK>, p);
+}
+
+template <class T, int THREADS>
+cudaError_t launch_lp_size(const LpParams &p, int sm_count, cudaStream_t st)
+{
+    return p.k > 0 ? launch_lp<T, THREADS, true>(p, sm_count, st) : launch_lp<T, THREADS, false>(p, sm_count, st);
 }
 
 template <class T>
 cudaError_t launch_lp_type(const LpParams &p, int sm_count, cudaStream_t st)
 {
-    return p.k > 0 ? launch_lp<T, 512, true>(p, sm_count, st) : launch_lp<T, 512, false>(p, sm_count, st);
+    // Short rows on small CTAs, eight to an SM: what a CTA does besides reading
+    // (barriers, the search, the ranking) is then spread over more rows.
+    const bool small = p.N <= kShortBatches * 128 * kUnroll * LpType<T>::VE;
+    return small ? launch_lp_size<T, 128>(p, sm_count, st) : launch_lp_size<T, 512>(p, sm_count, st);
 }
 
 } // namespace
