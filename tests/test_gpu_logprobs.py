@@ -141,6 +141,25 @@ def test_extreme_values():
     check(x, t, 3, wq.wq_logprobs(x, t, 3))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_maxima_far_from_zero(dtype):
+    """Maxima so large that 200 below them is the same 16-bit value, and so low
+    that nothing but -inf is below them."""
+    big, low = (6e4, -65504.0) if dtype == torch.float16 else (1e30, torch.finfo(dtype).min)
+    x = torch.zeros(6, 9000, dtype=dtype, device=dev())
+    x[0, 5] = big
+    x[1] = -math.inf
+    x[1, ::3] = low
+    x[2] = -big
+    x[2, 7] = -0.9 * big
+    x[3] = torch.linspace(1000, 1100, 9000, device=dev()).to(dtype)
+    x[4] = torch.linspace(-1100, -1000, 9000, device=dev()).to(dtype)
+    x[5] = low
+    x[5, 8000] = 0.97 * low
+    t = torch.tensor([5, 3, 7, 8999, 8999, 8000], dtype=torch.int32, device=dev())
+    check(x, t, 5, wq.wq_logprobs(x, t, 5))
+
+
 def test_zeros_of_both_signs_are_equal():
     x = torch.full((1, 300), -1.0, device=dev())
     x[0, 5], x[0, 9], x[0, 200] = -0.0, 0.0, -0.0

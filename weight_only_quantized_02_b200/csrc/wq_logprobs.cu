@@ -71,11 +71,60 @@ struct LpParams {
 __host__ __device__ constexpr int lp_accept(int k) { return k + k / 2 + 8; }
 static_assert(lp_accept(kTopkMaxK) <= kSortMax, "a cut list can be ranked");
 
+// ---- packed fp32 pairs ----
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b),
+                          z = *reinterpret_cast<unsigned long long *>(&c);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
+constexpr float kFarBelow = -200.f; // exp(-200) is 0 in fp32: masked and far logits add nothing, and 0 * -inf never forms
+
+__device__ __forceinline__ float2 cut2(float2 d) // NaN stays NaN
+{
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.x) : "f"(kFarBelow));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.y) : "f"(kFarBelow));
+    return d;
+}
+
+// Far below m, and by a margin that 16-bit formats resolve whatever m is.
+__device__ __forceinline__ float far_below(float m) { return m + kFarBelow - 0.02f * fabsf(m); }
+
 template <class T>
 struct LpType;
 template <>
 struct LpType<__nv_bfloat16> {
     static constexpr int VE = 8;
+    // A pair's differences from the maximum m, far ones cut short: the pair is
+    // held above `floor`, a pair far enough below m that what is cut counts for
+    // nothing, which costs one instruction.  There is such a value from
+    // m >= kFloorFrom on.
+    static constexpr float kFloorFrom = -3e38f;
+    static __device__ __forceinline__ uint32_t floor(float m)
+    {
+        const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rd(fmaxf(far_below(m), -3.38e38f)));
+        return h | (h << 16);
+    }
+    static __device__ __forceinline__ float2 diff(const uint4 &v, int i, float2 nm, uint32_t fl)
+    {
+        uint32_t w;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w) : "r"((&v.x)[i]), "r"(fl));
+        return add2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), nm);
+    }
     // largest of a vector, NaN if it holds one
     static __device__ __forceinline__ float vmax(const uint4 &v)
     {
@@ -96,6 +145,18 @@ struct LpType<__nv_bfloat16> {
 template <>
 struct LpType<__half> {
     static constexpr int VE = 8;
+    static constexpr float kFloorFrom = -6e4f;
+    static __device__ __forceinline__ uint32_t floor(float m)
+    {
+        const uint32_t h = __half_as_ushort(__float2half_rd(far_below(m)));
+        return h | (h << 16);
+    }
+    static __device__ __forceinline__ float2 diff(const uint4 &v, int i, float2 nm, uint32_t fl)
+    {
+        uint32_t w;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(w) : "r"((&v.x)[i]), "r"(fl));
+        return add2(__half22float2(*reinterpret_cast<const __half2 *>(&w)), nm);
+    }
     static __device__ __forceinline__ float vmax(const uint4 &v)
     {
         uint32_t a, b;
@@ -115,6 +176,12 @@ struct LpType<__half> {
 template <>
 struct LpType<float> {
     static constexpr int VE = 4;
+    static constexpr float kFloorFrom = -INFINITY; // each difference is cut by itself
+    static __device__ __forceinline__ uint32_t floor(float) { return 0; }
+    static __device__ __forceinline__ float2 diff(const uint4 &v, int i, float2 nm, uint32_t)
+    {
+        return cut2(add2(pair(v, i), nm));
+    }
     static __device__ __forceinline__ float vmax(const uint4 &v)
     {
         float a, b;
@@ -159,13 +226,19 @@ constexpr uint32_t kOrderNan = 0xFFFFFFFFu;
 // ---------------------------------------------------------------------------
 // Running softmax sums
 // ---------------------------------------------------------------------------
-constexpr float kFarBelow = -200.f; // exp(-200) is 0 in fp32: masked and far logits add nothing, and 0 * -inf never forms
 
 __device__ __forceinline__ float diff_clamped(float x, float m) // NaN stays NaN
 {
     float d = x - m;
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(kFarBelow));
     return d;
+}
+
+__device__ __forceinline__ float exp_2(float t)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e;
 }
 
 __device__ __forceinline__ float exp_nat(float d)
@@ -194,20 +267,6 @@ __device__ __forceinline__ void merge(Sums &a, Sums b)
     rescale(b, m);
     a.s += b.s;
     a.w += b.w;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b);
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return *reinterpret_cast<float2 *>(&r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b),
-                          z = *reinterpret_cast<unsigned long long *>(&c);
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return *reinterpret_cast<float2 *>(&r);
 }
 
 // ---------------------------------------------------------------------------
@@ -253,16 +312,24 @@ __device__ __forceinline__ uint32_t bound_of_threads(uint32_t mine, uint32_t top
 {
     if (__syncthreads_count(mine != 0) < k)
         return 0;
-    uint32_t lo = 0, hi = top; // at least k reach lo; fewer than k are above hi
+    // from the top down in growing steps (the maxima of many logits lie close
+    // together), then by halves
+    uint32_t lo = 0, hi = top; // at least k reach lo; fewer than k reach anything above hi
+    uint32_t step = 1u << 20;
     while (lo < hi) {
-        const uint32_t mid = hi - (hi - lo) / 2; // above lo
+        uint32_t mid = hi - (hi - lo) / 2; // above lo
+        if (lo == 0 && step < hi - mid)
+            mid = hi - step;
         const int c = __syncthreads_count(mine >= mid);
         if (c >= k && c <= lp_accept(k))
             return mid;
-        if (c < k)
+        if (c < k) {
             hi = mid - 1;
-        else
+            if (step < (1u << 30))
+                step <<= 1;
+        } else {
             lo = mid;
+        }
     }
     return lo;
 }
@@ -578,17 +645,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             rescale(a, bm);
         float2 s2 = make_float2(0.f, 0.f), w2 = s2;
         const float2 nm = make_float2(-a.m, -a.m);
+        const uint32_t fl = L::floor(a.m);
+        auto add = [&](bool fast) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
             for (int i = 0; i < VE / 2; ++i) {
-                float2 d = add2(L::pair(cur[u], i), nm);
-                asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.x) : "f"(kFarBelow));
-                asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.y) : "f"(kFarBelow));
-                const float2 e = make_float2(exp_nat(d.x), exp_nat(d.y));
+                const float2 d = fast ? L::diff(cur[u], i, nm, fl) : cut2(add2(L::pair(cur[u], i), nm));
+                const float2 t = mul2(d, make_float2(1.4426950408889634f, 1.4426950408889634f));
+                const float2 e = make_float2(exp_2(t.x), exp_2(t.y));
                 s2 = add2(s2, e);
                 w2 = fma2(e, d, w2);
             }
+        };
+        if (a.m >= L::kFloorFrom)
+            add(true);
+        else
+            add(false);
         a.s += s2.x + s2.y;
         a.w += w2.x + w2.y;
 
