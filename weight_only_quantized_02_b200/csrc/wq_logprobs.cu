@@ -26,8 +26,9 @@
 // thread knows the largest of the logits it read; a value that the maxima of at
 // least k threads reach (and of few more: a search with one block-wide count a
 // step) is reached by at least k logits, and only those threads' logits can be
-// among the k largest.  Their few vectors are read again, by all threads
-// together, out of L2, and what reaches the value is kept and ranked.  Where more
+// among the k largest; of those, the runs of vectors whose largest (kept in shared
+// memory, at most 32 a thread) reaches it.  They are read again, by all threads
+// together, and what reaches the value is kept and ranked.  Where more
 // reaches it than the list holds (rows of few distinct values, masks) the k-th
 // largest value is found by counting over those vectors, everything above it
 // kept, and of the logits equal to it the first in the row, by a scan that ends
@@ -53,6 +54,8 @@ namespace {
 constexpr int kUnroll = 4;     // 16-byte vectors per thread and batch
 constexpr int kSortMax = 192;  // candidates ranked by counting without a cut first
 constexpr int kListMax = 1024; // candidates of a CTA
+constexpr int kChosenMax = 1024; // runs of vectors read again
+constexpr int kRuns = 32;      // runs of a thread, at most
 constexpr int kLpMaxCluster = 8;
 constexpr int kShortBatches = 4; // rows of at most this many batches of a 128-thread CTA go to one
 
@@ -62,6 +65,7 @@ struct LpParams {
     const void *logits;
     long long ld;
     int M, N, k, C, slice; // slice: elements per CTA, a multiple of the vector
+    int run_batches;       // batches of a run
     const int32_t *tokens;
     float *logprob, *entropy, *top;
     int32_t *top_idx;
@@ -381,6 +385,7 @@ __device__ __forceinline__ void rank_into(const key_t64 *src, int n, int k, key_
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const key_t64 mine = src[i];
         int above = 0;
+#pragma unroll 8
         for (int j = 0; j < n; ++j)
             above += src[j] > mine;
         if (above < k)
@@ -389,7 +394,6 @@ __device__ __forceinline__ void rank_into(const key_t64 *src, int n, int k, key_
     __syncthreads();
 }
 
-template <int THREADS>
 struct LpShared {
     key_t64 list[kListMax];  // candidates
     key_t64 cut[kSortMax];   // a list cut back before it is ranked
@@ -397,7 +401,9 @@ struct LpShared {
     key_t64 others[kLpMaxCluster * kTopkMaxK];
     Sums warp_sums[32];
     Sums sums; // this CTA's
-    uint16_t chosen[THREADS]; // threads whose logits may be among the k largest
+    // runs of vectors that may hold one of the k largest: the thread that read
+    // them, and the run's number among its own in the upper half
+    uint32_t chosen[kChosenMax];
     int chosen_count, count, cut_count, list_count[2];
     int warp_count[32];
 };
@@ -443,29 +449,45 @@ struct Slice {
     }
 };
 
-// Elements of the vectors of the chosen threads and of the edges whose order32
-// is above o (at least o with or_equal): f(order32, index) for each, from any
-// thread.  The vectors come out of L2.
+// Elements of the chosen runs of `per` vectors and of the edges whose order32 is
+// above o (at least o with or_equal): f(order32, index) for each, from any
+// thread.
 template <class T, int THREADS, class Shared, class F>
-__device__ __forceinline__ void each_above(const Slice<T, THREADS> &sl, const Shared &sh, uint32_t o, bool or_equal, F f)
+__device__ __forceinline__ void each_above(const Slice<T, THREADS> &sl, const Shared &sh, int per, uint32_t o,
+                                           bool or_equal, F f)
 {
     using L = LpType<T>;
     constexpr int VE = L::VE;
-    const int per = (sl.nv + THREADS - 1) / THREADS; // vectors of a thread, at most
     const int items = sh.chosen_count * per;
-    for (int i = threadIdx.x; i < items; i += THREADS) {
-        const int v = (i % per) * THREADS + sh.chosen[i / per];
-        if (v >= sl.nv)
-            continue;
-        const uint4 q = __ldg(sl.vec() + v);
+    const float of = value32(o); // a NaN passes, and lets everything pass
+    constexpr int G = 4;         // vectors in flight
+    for (int i0 = threadIdx.x; i0 < items; i0 += G * THREADS) {
+        uint4 q[G];
+        int v[G];
 #pragma unroll
-        for (int j = 0; j < VE / 2; ++j) {
-            const float2 x = L::pair(q, j);
-            const uint32_t a = order32(x.x), b = order32(x.y);
-            if (a > o || (or_equal && a == o))
-                f(a, sl.v0 + v * VE + 2 * j);
-            if (b > o || (or_equal && b == o))
-                f(b, sl.v0 + v * VE + 2 * j + 1);
+        for (int g = 0; g < G; ++g) {
+            const int i = i0 + g * THREADS, c = i / per;
+            v[g] = sl.nv;
+            if (i < items) {
+                const uint32_t run = sh.chosen[c];
+                v[g] = ((int)(run >> 16) * per + i - c * per) * THREADS + (int)(run & 0xFFFFu);
+            }
+            if (v[g] < sl.nv)
+                q[g] = __ldg(sl.vec() + v[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (v[g] >= sl.nv || L::vmax(q[g]) < of)
+                continue;
+#pragma unroll
+            for (int j = 0; j < VE / 2; ++j) {
+                const float2 x = L::pair(q[g], j);
+                const uint32_t a = order32(x.x), b = order32(x.y);
+                if (a > o || (or_equal && a == o))
+                    f(a, sl.v0 + v[g] * VE + 2 * j);
+                if (b > o || (or_equal && b == o))
+                    f(b, sl.v0 + v[g] * VE + 2 * j + 1);
+            }
         }
     }
     const int e = sl.edge();
@@ -534,17 +556,40 @@ __device__ __noinline__ void first_equal(const Slice<T, THREADS> &sl, Shared &sh
 }
 
 // The slice's k best, in order, into sh.best.  mine: order32 that the largest
-// logit this thread read reaches, 0 if it read none; top: no logit is above it.
+// logit this thread read reaches, 0 if it read none; top: no logit is above it;
+// runs: the largest of each run of per_run vectors this thread read, THREADS
+// apart (nan: one may be hidden in them).
 template <class T, int THREADS, class Shared>
-__device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared &sh, uint32_t mine, uint32_t top, int k)
+__device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared &sh, uint32_t mine, uint32_t top, int k,
+                                            const float *runs, int per_run, bool nan)
 {
     if (threadIdx.x == 0)
         sh.chosen_count = sh.count = 0;
     const uint32_t bound = bound_of_threads(mine, min(top, kOrderInf), k); // has a barrier
-    if (mine != 0 && mine >= bound)
-        sh.chosen[atomicAdd(&sh.chosen_count, 1)] = (uint16_t)threadIdx.x;
+    const int all = (sl.nv + THREADS - 1) / THREADS; // vectors of a thread, at most
+    const bool chosen = mine != 0 && mine >= bound;
+    if (chosen) {
+        const float of = value32(bound);
+        for (int i = 0; i * per_run < all; ++i)
+            if (nan || !(runs[i * THREADS] < of)) {
+                const int at = atomicAdd(&sh.chosen_count, 1);
+                if (at < kChosenMax)
+                    sh.chosen[at] = (uint32_t)i << 16 | threadIdx.x;
+            }
+    }
     __syncthreads();
-    each_above(sl, sh, bound, true, [&](uint32_t o, int idx) {
+    int per = per_run;
+    if (sh.chosen_count > kChosenMax) { // too many runs: the chosen threads' whole columns
+        per = all;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            sh.chosen_count = 0;
+        __syncthreads();
+        if (chosen)
+            sh.chosen[atomicAdd(&sh.chosen_count, 1)] = threadIdx.x;
+        __syncthreads();
+    }
+    each_above(sl, sh, per, bound, true, [&](uint32_t o, int idx) {
         const int at = atomicAdd(&sh.count, 1);
         if (at < kListMax)
             sh.list[at] = ((key_t64)o << 32) | (uint32_t)~idx;
@@ -558,7 +603,7 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
         while (lo < hi) {
             const uint32_t mid = hi - (hi - lo) / 2;
             int c = 0;
-            each_above(sl, sh, mid, true, [&](uint32_t, int) { ++c; });
+            each_above(sl, sh, per, mid, true, [&](uint32_t, int) { ++c; });
             if (block_sum(c, sh.list_count, slot) >= k)
                 lo = mid;
             else
@@ -568,7 +613,7 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
         if (threadIdx.x == 0)
             sh.count = 0;
         __syncthreads();
-        each_above(sl, sh, lo, false, [&](uint32_t o, int idx) { // fewer than k
+        each_above(sl, sh, per, lo, false, [&](uint32_t o, int idx) { // fewer than k
             sh.list[atomicAdd(&sh.count, 1)] = ((key_t64)o << 32) | (uint32_t)~idx;
         });
         __syncthreads();
@@ -585,7 +630,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
 {
     using L = LpType<T>;
     constexpr int VE = L::VE, B = THREADS * kUnroll; // vectors per batch
-    __shared__ LpShared<THREADS> sh;
+    __shared__ LpShared sh;
+    extern __shared__ float s_runs[]; // [kRuns][THREADS] (TOPK)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = p.C > 1 ? (int)cluster_rank() : 0;
     const int m = blockIdx.x / p.C, k = p.k;
@@ -633,6 +679,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         a.w = a.s * d;
     }
 
+    int run = 0, in_run = 0; // of this batch
+    float run_max = -INFINITY;
     for (int b = 0; b < nv; b += B) {
         if (b + B < nv)
             load(b + B, nxt);
@@ -641,6 +689,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         for (int u = 1; u < kUnroll; ++u)
             bm = fmaxf(bm, L::vmax(cur[u]));
         largest = fmaxf(largest, bm);
+        if constexpr (TOPK) {
+            run_max = fmaxf(run_max, bm);
+            s_runs[run * THREADS + threadIdx.x] = run_max;
+            if (++in_run == p.run_batches) {
+                ++run;
+                in_run = 0;
+                run_max = -INFINITY;
+            }
+        }
         if (bm > a.m)
             rescale(a, bm);
         float2 s2 = make_float2(0.f, 0.f), w2 = s2;
@@ -672,9 +729,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
 
     // order32 of this thread's largest, or, where a NaN sum tells of a NaN or +inf
     // in it, what it reaches at least
+    const bool a_nan = a.s != a.s;
     uint32_t mine = 0;
     if (edge >= 0 || (int)threadIdx.x < nv)
-        mine = a.s != a.s ? kOrderInf : order32(largest);
+        mine = a_nan ? kOrderInf : order32(largest);
 
     // ---- the CTA's sums: lanes, then warps, in a fixed order ----
 #pragma unroll
@@ -691,11 +749,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     if (lane == 0)
         sh.warp_sums[warp] = a;
     __syncthreads(); // also: every candidate is in the list
-    Sums t = sh.warp_sums[0];
-    for (int i = 1; i < THREADS / 32; ++i)
-        merge(t, sh.warp_sums[i]);
+    constexpr int W = THREADS / 32;
+    Sums t = sh.warp_sums[lane & (W - 1)]; // every warp, the same sums in the same order
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+        Sums x;
+        x.m = __shfl_xor_sync(0xffffffffu, t.m, o);
+        x.s = __shfl_xor_sync(0xffffffffu, t.s, o);
+        x.w = __shfl_xor_sync(0xffffffffu, t.w, o);
+        Sums lo = (lane & o) ? x : t, hi = (lane & o) ? t : x;
+        merge(lo, hi);
+        t = lo;
+    }
     if constexpr (TOPK)
-        select_best(sl, sh, mine, t.s != t.s ? kOrderNan : order32(t.m), k);
+        select_best(sl, sh, mine, t.s != t.s ? kOrderNan : order32(t.m), k, s_runs + threadIdx.x,
+                    p.run_batches * kUnroll, a_nan);
     if (p.C > 1) {
         if (threadIdx.x == 0)
             sh.sums = t;
@@ -761,6 +829,13 @@ cudaError_t launch_lp(LpParams p, int sm_count, cudaStream_t st)
         C *= 2;
     p.C = C;
     p.slice = ((p.N + C - 1) / C + VE - 1) / VE * VE;
+    const int batches = (p.slice + THREADS * kUnroll * VE - 1) / (THREADS * kUnroll * VE);
+    p.run_batches = (batches + kRuns - 1) / kRuns;
+    const int runs = p.run_batches ? (batches + p.run_batches - 1) / p.run_batches : 0;
+    const size_t smem = TOPK ? (size_t)runs * THREADS * sizeof(float) : 0;
+    const cudaError_t e = kernel_setup((const void *)logprobs_kernel<T, THREADS, TOPK>, smem, 0, 0, nullptr);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -773,6 +848,7 @@ cudaError_t launch_lp(LpParams p, int sm_count, cudaStream_t st)
     cfg.numAttrs = C > 1 ? 2 : 1;
     cfg.gridDim = dim3((unsigned)p.M * C);
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS, TOPK>, p);
 }
@@ -789,7 +865,7 @@ cudaError_t launch_lp_type(const LpParams &p, int sm_count, cudaStream_t st)
     // Short rows on small CTAs, eight to an SM: what a CTA does besides reading
     // (barriers, the search, the ranking) is then spread over more rows.
     const bool small = p.N <= kShortBatches * 128 * kUnroll * LpType<T>::VE;
-    return small ? launch_lp_size<T, 128>(p, sm_count, st) : launch_lp_size<T, 512>(p, sm_count, st);
+    return small ? launch_lp_size<T, 128>(p, sm_count, st) : launch_lp_size<T, 256>(p, sm_count, st);
 }
 
 } // namespace
@@ -798,7 +874,7 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int M, int N, long lo
                             float *logprob, float *entropy, float *top, int32_t *top_idx, int sm_count,
                             cudaStream_t st)
 {
-    LpParams p{logits, ld, M, N, k, 1, N, tokens, logprob, entropy, top, top_idx};
+    LpParams p{logits, ld, M, N, k, 1, N, 1, tokens, logprob, entropy, top, top_idx};
     switch (dtype) {
     case WQ_DTYPE_BF16: return launch_lp_type<__nv_bfloat16>(p, sm_count, st);
     case WQ_DTYPE_F16: return launch_lp_type<__half>(p, sm_count, st);
