@@ -273,6 +273,23 @@ __device__ __forceinline__ void merge(Sums &a, Sums b)
     a.w += b.w;
 }
 
+// The sums of lanes 0 .. n-1 (a power of two, repeated over the warp) for every
+// lane, each pair with the lower lane's first, so that all form the same sum.
+__device__ __forceinline__ Sums butterfly(Sums t, int n)
+{
+    const int lane = threadIdx.x & 31;
+    for (int o = n >> 1; o > 0; o >>= 1) {
+        Sums x;
+        x.m = __shfl_xor_sync(0xffffffffu, t.m, o);
+        x.s = __shfl_xor_sync(0xffffffffu, t.s, o);
+        x.w = __shfl_xor_sync(0xffffffffu, t.w, o);
+        Sums lo = (lane & o) ? x : t, hi = (lane & o) ? t : x;
+        merge(lo, hi);
+        t = lo;
+    }
+    return t;
+}
+
 // ---------------------------------------------------------------------------
 // Cluster (distributed shared memory)
 // ---------------------------------------------------------------------------
@@ -405,6 +422,7 @@ struct LpShared {
     // them, and the run's number among its own in the upper half
     uint32_t chosen[kChosenMax];
     int chosen_count, count, cut_count, list_count[2];
+    int place[kTopkMaxK];
     int warp_count[32];
 };
 
@@ -459,6 +477,7 @@ __device__ __forceinline__ void each_above(const Slice<T, THREADS> &sl, const Sh
     using L = LpType<T>;
     constexpr int VE = L::VE;
     const int items = sh.chosen_count * per;
+    const float inv = 1.f / (float)per;
     const float of = value32(o); // a NaN passes, and lets everything pass
     constexpr int G = 4;         // vectors in flight
     for (int i0 = threadIdx.x; i0 < items; i0 += G * THREADS) {
@@ -466,7 +485,9 @@ __device__ __forceinline__ void each_above(const Slice<T, THREADS> &sl, const Sh
         int v[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const int i = i0 + g * THREADS, c = i / per;
+            // i / per: i < 2^18, so (i + 1/2) / per is off by less than its distance
+            // to a whole number, 1 / (2 per)
+            const int i = i0 + g * THREADS, c = (int)(((float)i + 0.5f) * inv);
             v[g] = sl.nv;
             if (i < items) {
                 const uint32_t run = sh.chosen[c];
@@ -570,12 +591,20 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
     const bool chosen = mine != 0 && mine >= bound;
     if (chosen) {
         const float of = value32(bound);
-        for (int i = 0; i * per_run < all; ++i)
-            if (nan || !(runs[i * THREADS] < of)) {
-                const int at = atomicAdd(&sh.chosen_count, 1);
+        const int n = (all + per_run - 1) / per_run;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            uint32_t hit = 0; // eight at a time: the loads overlap
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n)
+                    hit |= (uint32_t)(nan || !(runs[(i0 + i) * THREADS] < of)) << i;
+            if (hit == 0)
+                continue;
+            int at = atomicAdd(&sh.chosen_count, __popc(hit));
+            for (; hit; hit &= hit - 1, ++at)
                 if (at < kChosenMax)
-                    sh.chosen[at] = (uint32_t)i << 16 | threadIdx.x;
-            }
+                    sh.chosen[at] = (uint32_t)(i0 + __ffs(hit) - 1) << 16 | threadIdx.x;
+        }
     }
     __syncthreads();
     int per = per_run;
@@ -735,32 +764,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         mine = a_nan ? kOrderInf : order32(largest);
 
     // ---- the CTA's sums: lanes, then warps, in a fixed order ----
+    {
+        float mx = a.m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Sums x;
-        x.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-        x.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-        x.w = __shfl_xor_sync(0xffffffffu, a.w, o);
-        // the lower lane's half first on both sides, so that both form the same sum
-        Sums lo = (lane & o) ? x : a, hi = (lane & o) ? a : x;
-        merge(lo, hi);
-        a = lo;
+        for (int o = 16; o > 0; o >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        rescale(a, mx);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) { // both sides of an exchange form the same sum
+            a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+            a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+        }
     }
     if (lane == 0)
         sh.warp_sums[warp] = a;
     __syncthreads(); // also: every candidate is in the list
     constexpr int W = THREADS / 32;
     Sums t = sh.warp_sums[lane & (W - 1)]; // every warp, the same sums in the same order
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-        Sums x;
-        x.m = __shfl_xor_sync(0xffffffffu, t.m, o);
-        x.s = __shfl_xor_sync(0xffffffffu, t.s, o);
-        x.w = __shfl_xor_sync(0xffffffffu, t.w, o);
-        Sums lo = (lane & o) ? x : t, hi = (lane & o) ? t : x;
-        merge(lo, hi);
-        t = lo;
-    }
+    t = butterfly(t, W);
     if constexpr (TOPK)
         select_best(sl, sh, mine, t.s != t.s ? kOrderNan : order32(t.m), k, s_runs + threadIdx.x,
                     p.run_batches * kUnroll, a_nan);
@@ -768,18 +789,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         if (threadIdx.x == 0)
             sh.sums = t;
         cluster_sync();
-        t = Sums{-FLT_MAX, 0.f, 0.f};
-        for (int c = 0; c < p.C; ++c) {
-            const uint32_t at = cluster_addr(&sh.sums, c);
-            Sums x;
-            x.m = cluster_ld_f32(at);
-            x.s = cluster_ld_f32(at + 4);
-            x.w = cluster_ld_f32(at + 8);
-            merge(t, x);
+        { // lane c holds CTA c's sums (p.C is a power of two)
+            const uint32_t at = cluster_addr(&sh.sums, lane & (p.C - 1));
+            t.m = cluster_ld_f32(at);
+            t.s = cluster_ld_f32(at + 4);
+            t.w = cluster_ld_f32(at + 8);
         }
         if constexpr (TOPK)
             for (int i = threadIdx.x; i < p.C * k; i += THREADS)
                 sh.others[i] = cluster_ld_u64(cluster_addr(&sh.best[i % k], i / k));
+        t = butterfly(t, p.C);
         cluster_sync(); // no CTA leaves while another reads its shared memory
     }
     const float log_s = logf(t.s);
@@ -790,15 +809,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             p.entropy[m] = log_s - t.w / t.s;
     }
     if constexpr (TOPK) {
-        for (int i = threadIdx.x; i < k; i += THREADS) {
-            const key_t64 key = sh.best[i];
-            if (key == 0)
-                continue; // this slice is shorter than k
-            int at = i;
-            for (int c = 0; c < p.C && p.C > 1; ++c) {
+        // an entry's place: its own list's, and the entries above it in the others
+        if (p.C > 1) {
+            for (int i = threadIdx.x; i < k; i += THREADS)
+                sh.place[i] = i;
+            __syncthreads();
+            for (int i = threadIdx.x; i < p.C * k; i += THREADS) {
+                const int c = i / k, e = i - c * k;
                 if (c == rank)
                     continue;
-                const key_t64 *o = sh.others + c * k;
+                const key_t64 key = sh.best[e], *o = sh.others + c * k;
                 int lo = 0, hi = k; // entries of a descending list above key
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
@@ -807,9 +827,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
                     else
                         hi = mid;
                 }
-                at += lo;
+                if (lo)
+                    atomicAdd(&sh.place[e], lo);
             }
-            if (at < k) {
+            __syncthreads();
+        }
+        for (int i = threadIdx.x; i < k; i += THREADS) {
+            const key_t64 key = sh.best[i];
+            const int at = p.C > 1 ? sh.place[i] : i;
+            if (key != 0 && at < k) { // 0: this slice is shorter than k
                 p.top[(size_t)m * k + at] = (value32((uint32_t)(key >> 32)) - t.m) - log_s;
                 p.top_idx[(size_t)m * k + at] = (int32_t)~(uint32_t)key;
             }
