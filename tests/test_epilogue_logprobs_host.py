@@ -107,17 +107,19 @@ def test_binding_refuses_before_the_library():
 
 
 def test_binding_checks_the_operands():
-    M, N, dt, cpu = 4, 64, torch.bfloat16, torch.device("cpu")
+    M, N, dt, cpu = 4, 64, torch.bfloat16, -1
     good = torch.zeros(M, N, dtype=dt)
     assert wq._rows(good, (M, N), dt, cpu, "t") == N
     assert wq._rows(torch.zeros(M, 2 * N, dtype=dt)[:, 3:N + 3], (M, N), dt, cpu, "t") == 2 * N
     refused(DTYPE, wq._rows, good.float(), (M, N), dt, cpu, "t")
     refused(SHAPE, wq._rows, good[:, :60], (M, N), dt, cpu, "t")
     refused(SHAPE, wq._rows, torch.zeros(N, M, dtype=dt).t(), (M, N), dt, cpu, "t")
-    refused(SHAPE, wq._rows, good, (M, N), dt, torch.device("meta"), "t")
+    refused(SHAPE, wq._rows, good, (M, N), dt, 1, "t")
     refused(DTYPE, wq._vector, torch.zeros(4, dtype=torch.int64), 4, torch.int32, cpu, "t")
     refused(SHAPE, wq._vector, torch.zeros(8, dtype=torch.int32)[::2], 4, torch.int32, cpu, "t")
-    refused(SHAPE, wq._logprob_outputs, 4, None, -1, cpu, "t")
+    refused(SHAPE, wq._vector, torch.zeros(4, dtype=torch.int32), 4, torch.int32, 0, "t")
+    refused(SHAPE, wq._logprob_outputs, good, 4, None, -1, cpu, "t")
+    refused(SHAPE, wq._scratch, torch.zeros(8), 0, "t")
 
 
 def test_new_statuses_have_names():

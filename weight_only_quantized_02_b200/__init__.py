@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -292,89 +293,140 @@ class _Epilogue(ctypes.Structure):
                 ("ld_mul", ctypes.c_int64), ("ld_residual", ctypes.c_int64), ("act", ctypes.c_int)]
 
 
+# What follows is on the path of a decode step's smallest calls, which take less
+# time on the GPU than a call takes here: pointers go to the library as plain
+# integers, tensors are asked once for what is looked at twice, and each thread
+# keeps one epilogue struct (the library copies it before it returns).
+class _PerThread(threading.local):
+    def __init__(self):
+        self.epilogue = _Epilogue()
+        self.epilogue_ref = ctypes.byref(self.epilogue)
+
+
+_per_thread = _PerThread()
+
+
 def _refuse(status: int, what: str) -> None:
     raise WQError(status, what)
 
 
-def _rows(t: torch.Tensor, shape, dtype, device, what: str) -> int:
-    """Row stride in elements of a 2-D operand whose rows are contiguous."""
+def _rows(t: torch.Tensor, shape, dtype, device: int, what: str) -> int:
+    """Row stride in elements of a 2-D operand whose rows are contiguous, on
+    the CUDA device of that index (-1: the CPU)."""
     if t.dtype != dtype:
         _refuse(-13, f"{what} is {t.dtype}, not {dtype}")
-    if tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
-        _refuse(-2, f"{what} {tuple(t.shape)} strides {tuple(t.stride())}, not rows of {tuple(shape)}")
-    if t.device != device:
-        _refuse(-2, f"{what} is on {t.device}, not {device}")
-    return t.stride(0)
+    if t.shape != shape:
+        _refuse(-2, f"{what} {tuple(t.shape)}, not {tuple(shape)}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        _refuse(-2, f"{what}: strides {(ld, step)}, not rows of consecutive elements")
+    if t.get_device() != device:
+        _refuse(-2, f"{what} is on {t.device}")
+    return ld
 
 
-def _vector(t: torch.Tensor, n: int, dtype, device, what: str) -> None:
+def _vector(t: torch.Tensor, n: int, dtype, device: int, what: str) -> int:
+    """Address of a contiguous vector of n elements."""
     if t.dtype != dtype:
         _refuse(-13, f"{what} is {t.dtype}, not {dtype}")
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         _refuse(-2, f"{what} {tuple(t.shape)} strides {tuple(t.stride())}, not contiguous ({n},)")
-    if t.device != device:
-        _refuse(-2, f"{what} is on {t.device}, not {device}")
+    if t.get_device() != device:
+        _refuse(-2, f"{what} is on {t.device}")
+    return t.data_ptr()
+
+
+# The handle of a device's current stream; torch.cuda.current_stream() makes an
+# object for it, which takes longer than the launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 class _on:
-    """Makes x's device and the stream the call runs on (a torch stream or a
-    raw handle; None: the device's current one) current for the block, so that
-    outputs are allocated for the stream that writes them.  Yields the
-    stream's handle."""
+    """Makes a device and the stream a call runs on (a torch stream or a raw
+    handle; None: the device's current one) current for the block, so that
+    outputs are allocated for the stream that writes them.  Yields the stream's
+    handle."""
 
-    def __init__(self, device: torch.device, stream):
-        if device.type != "cuda":
-            _refuse(-2, f"tensors on {device}, not on a CUDA device")
-        self._contexts = ()
-        if stream is not None or torch.cuda.current_device() != device.index:
-            if stream is not None and not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self._contexts = (torch.cuda.device(device), torch.cuda.stream(stream))
+    def __init__(self, device: int, stream):
+        self._index = device
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self._contexts = (torch.cuda.device(device), torch.cuda.stream(stream))
 
-    def __enter__(self):
+    def __enter__(self) -> int:
         for c in self._contexts:
             c.__enter__()
-        return _s(None)
+        return _raw_stream(self._index)
 
     def __exit__(self, *exc):
         for c in reversed(self._contexts):
             c.__exit__(*exc)
 
 
-def _layer_input(x: torch.Tensor, pw: PackedWeight, dtype, what: str) -> None:
+def _run_on(device: int, stream, call):
+    """call(stream handle) with the tensors' device and the stream current."""
+    if device < 0:
+        _refuse(-2, "the tensors are not on a CUDA device")
+    if stream is None and torch.cuda.current_device() == device:
+        return call(_raw_stream(device))
+    with _on(device, stream) as s:
+        return call(s)
+
+
+def _layer_input(x: torch.Tensor, pw: PackedWeight, dtype, what: str):
+    """(M, device index) of a layer's input."""
     if x.dtype != dtype:
         _refuse(-13, f"{what}: x is {x.dtype}, not {dtype}")
     if x.dim() != 2 or x.shape[1] != pw.K or not x.is_contiguous():
         _refuse(-2, f"{what}: x {tuple(x.shape)} strides {tuple(x.stride())}, not contiguous [M][{pw.K}]")
-    if pw.wq.device != x.device:
+    device = x.get_device()
+    if pw.wq.get_device() != device:
         _refuse(-2, f"{what}: x on {x.device}, the weight on {pw.wq.device}")
+    return x.shape[0], device
 
 
-def _scratch(ws: Optional[torch.Tensor], device, what: str):
+def _weight_pointers(pw: PackedWeight):
+    return pw.wq.data_ptr(), pw.scales.data_ptr(), None if pw.zeros is None else pw.zeros.data_ptr()
+
+
+def _scratch(ws: Optional[torch.Tensor], device: int, what: str):
     if ws is None:
         return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        _refuse(-2, f"{what}: a contiguous buffer on {device} is wanted")
-    return _p(ws), ws.numel() * ws.element_size()
+    if ws.get_device() != device or not ws.is_contiguous():
+        _refuse(-2, f"{what}: a contiguous buffer on the device of the other tensors is wanted")
+    return ws.data_ptr(), ws.nbytes
 
 
-def _epilogue(x, pw, bias, act, mul, residual, y, what):
-    M, dtype, dev = x.shape[0], x.dtype, x.device
-    e = _Epilogue(act=int(act))
-    if bias is not None:
-        _vector(bias, pw.N, dtype, dev, f"{what}: bias")
-        e.bias = bias.data_ptr()
-    if mul is not None:
-        e.ld_mul = _rows(mul, (M, pw.N), dtype, dev, f"{what}: mul")
-        e.mul = mul.data_ptr()
-    if residual is not None:
-        e.ld_residual = _rows(residual, (M, pw.N), dtype, dev, f"{what}: residual")
-        e.residual = residual.data_ptr()
-    if y is None:
-        y = torch.empty((M, pw.N), dtype=dtype, device=dev)
-    elif _rows(y, (M, pw.N), dtype, dev, f"{what}: y") != pw.N and M > 1:
-        _refuse(-2, f"{what}: y is not contiguous")
-    return e, y
+def _linear_epilogue(fn, what, x, pw, bias, act, mul, residual, y, dtype, stream, ws=None):
+    M, device = _layer_input(x, pw, dtype, what)
+    N = pw.N
+    shape = (M, N)
+    workspace = () if dtype == torch.float16 else _scratch(ws, device, f"{what}: ws")  # the fp16 form takes none
+
+    def call(s):
+        out = y
+        if out is None:
+            out = x.new_empty(shape)
+        elif _rows(out, shape, dtype, device, f"{what}: y") != N and M > 1:
+            _refuse(-2, f"{what}: y is not contiguous")
+        e = _per_thread.epilogue
+        e.act = act
+        e.bias = None if bias is None else _vector(bias, N, dtype, device, f"{what}: bias")
+        e.mul = e.residual = None
+        if mul is not None:
+            e.ld_mul = _rows(mul, shape, dtype, device, f"{what}: mul")
+            e.mul = mul.data_ptr()
+        if residual is not None:
+            e.ld_residual = _rows(residual, shape, dtype, device, f"{what}: residual")
+            e.residual = residual.data_ptr()
+        w, sc, z = _weight_pointers(pw)
+        rc = fn(x.data_ptr(), M, pw.K, w, sc, z, pw.group, N, _per_thread.epilogue_ref, out.data_ptr(), *workspace, s)
+        if rc != 0:
+            raise WQError(rc, what)
+        return out
+
+    return _run_on(device, stream, call)
 
 
 def wq_linear_epilogue(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor] = None,
@@ -385,13 +437,8 @@ def wq_linear_epilogue(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.T
     [M][K], bias [N], mul and residual [M][N] (rows may be strided), all bf16.
     y may be residual or mul themselves.  ws: this call's workspace (zeroed
     before its first use), else the registered one."""
-    _layer_input(x, pw, torch.bfloat16, "wq_linear_epilogue")
-    with _on(x.device, stream) as s:
-        e, y = _epilogue(x, pw, bias, act, mul, residual, y, "wq_linear_epilogue")
-        w, nbytes = _scratch(ws, x.device, "wq_linear_epilogue: ws")
-        _check(lib.wq_linear_epilogue(_p(x), x.shape[0], pw.K, _p(pw.wq), _p(pw.scales), _p(pw.zeros), pw.group, pw.N,
-                                      ctypes.byref(e), _p(y), w, nbytes, s), "wq_linear_epilogue")
-    return y
+    return _linear_epilogue(lib.wq_linear_epilogue, "wq_linear_epilogue", x, pw, bias, act, mul, residual, y,
+                            torch.bfloat16, stream, ws)
 
 
 def wq_linear_epilogue_f16(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor] = None,
@@ -400,25 +447,26 @@ def wq_linear_epilogue_f16(x: torch.Tensor, pw: PackedWeight, bias: Optional[tor
                            y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """wq_linear_epilogue with fp16 activations, operands and outputs (ws is
     not needed and not looked at)."""
-    _layer_input(x, pw, torch.float16, "wq_linear_epilogue_f16")
-    with _on(x.device, stream) as s:
-        e, y = _epilogue(x, pw, bias, act, mul, residual, y, "wq_linear_epilogue_f16")
-        _check(lib.wq_linear_epilogue_f16(_p(x), x.shape[0], pw.K, _p(pw.wq), _p(pw.scales), _p(pw.zeros), pw.group,
-                                          pw.N, ctypes.byref(e), _p(y), s), "wq_linear_epilogue_f16")
-    return y
+    return _linear_epilogue(lib.wq_linear_epilogue_f16, "wq_linear_epilogue_f16", x, pw, bias, act, mul, residual, y,
+                            torch.float16, stream)
 
 
 _LOGIT_DTYPES = {torch.bfloat16: WQ_DTYPE_BF16, torch.float16: WQ_DTYPE_F16, torch.float32: WQ_DTYPE_F32}
 
 
-def _logprob_outputs(M: int, tokens, k: int, device, what: str):
-    if tokens is not None:
-        _vector(tokens, M, torch.int32, device, f"{what}: tokens")
+def _logprob_outputs(like: torch.Tensor, M: int, tokens, k: int, device: int, what: str):
+    """The tokens' address (or None), the four outputs and their addresses."""
     if k < 0:
         _refuse(-2, f"{what}: k = {k}")
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
-    return (None if tokens is None else new((M,), torch.float32), new((M,), torch.float32),
-            new((M, k), torch.float32) if k else None, new((M, k), torch.int32) if k else None)
+    tp = None if tokens is None else _vector(tokens, M, torch.int32, device, f"{what}: tokens")
+    entropy = like.new_empty((M,), dtype=torch.float32)
+    logprob = entropy.new_empty((M,)) if tp else None
+    lp = logprob.data_ptr() if tp else None
+    if k == 0:
+        return tp, (logprob, entropy, None, None), (lp, entropy.data_ptr(), None, None)
+    top = entropy.new_empty((M, k))
+    idx = tokens.new_empty((M, k)) if tp else like.new_empty((M, k), dtype=torch.int32)
+    return tp, (logprob, entropy, top, idx), (lp, entropy.data_ptr(), top.data_ptr(), idx.data_ptr())
 
 
 def wq_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, k: int = 0, stream=None):
@@ -426,17 +474,25 @@ def wq_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, k: 
     [M][k] int32) of rows of logits (bf16, fp16 or fp32 [M][N], rows may be
     strided); fp32 but for the indices.  tokens int32 [M]; without them the
     first is None, with k = 0 the last two are."""
-    if logits.dtype not in _LOGIT_DTYPES:
+    dtype = _LOGIT_DTYPES.get(logits.dtype)
+    if dtype is None:
         _refuse(-13, f"wq_logprobs: logits are {logits.dtype}")
     if logits.dim() != 2:
         _refuse(-2, f"wq_logprobs: logits {tuple(logits.shape)}, not [M][N]")
     M, N = logits.shape
-    ld = _rows(logits, (M, N), logits.dtype, logits.device, "wq_logprobs: logits")
-    with _on(logits.device, stream) as s:
-        logprob, entropy, top, idx = _logprob_outputs(M, tokens, k, logits.device, "wq_logprobs")
-        _check(lib.wq_logprobs(_p(logits), _LOGIT_DTYPES[logits.dtype], M, N, ld, _p(tokens), k, _p(logprob),
-                               _p(entropy), _p(top), _p(idx), s), "wq_logprobs")
-    return logprob, entropy, top, idx
+    ld, step = logits.stride()
+    if step != 1 and N > 1:
+        _refuse(-2, f"wq_logprobs: logits' strides {(ld, step)}, not rows of consecutive elements")
+    device = logits.get_device()
+
+    def call(s):
+        tp, out, pointers = _logprob_outputs(logits, M, tokens, k, device, "wq_logprobs")
+        rc = lib.wq_logprobs(logits.data_ptr(), dtype, M, N, ld, tp, k, *pointers, s)
+        if rc != 0:
+            raise WQError(rc, "wq_logprobs")
+        return out
+
+    return _run_on(device, stream, call)
 
 
 def wq_linear_logprobs_workspace_bytes(M: int, N: int) -> int:
@@ -448,16 +504,19 @@ def wq_linear_logprobs(x: torch.Tensor, pw: PackedWeight, tokens: Optional[torch
     """wq_logprobs of the fp32 logits x . dequant(W)^T of a quantized
     vocabulary head; scratch a device buffer of at least
     wq_linear_logprobs_workspace_bytes(M, N) bytes, ws as wq_linear_epilogue."""
-    _layer_input(x, pw, torch.bfloat16, "wq_linear_logprobs")
-    M = x.shape[0]
-    with _on(x.device, stream) as s:
-        logprob, entropy, top, idx = _logprob_outputs(M, tokens, k, x.device, "wq_linear_logprobs")
-        sp, sbytes = _scratch(scratch, x.device, "wq_linear_logprobs: scratch")
-        w, nbytes = _scratch(ws, x.device, "wq_linear_logprobs: ws")
-        _check(lib.wq_linear_logprobs(_p(x), M, pw.K, _p(pw.wq), _p(pw.scales), _p(pw.zeros), pw.group, pw.N,
-                                      _p(tokens), k, _p(logprob), _p(entropy), _p(top), _p(idx), sp, sbytes, w, nbytes,
-                                      s), "wq_linear_logprobs")
-    return logprob, entropy, top, idx
+    M, device = _layer_input(x, pw, torch.bfloat16, "wq_linear_logprobs")
+    buffers = (*_scratch(scratch, device, "wq_linear_logprobs: scratch"),
+               *_scratch(ws, device, "wq_linear_logprobs: ws"))
+
+    def call(s):
+        tp, out, pointers = _logprob_outputs(x, M, tokens, k, device, "wq_linear_logprobs")
+        w, sc, z = _weight_pointers(pw)
+        rc = lib.wq_linear_logprobs(x.data_ptr(), M, pw.K, w, sc, z, pw.group, pw.N, tp, k, *pointers, *buffers, s)
+        if rc != 0:
+            raise WQError(rc, "wq_linear_logprobs")
+        return out
+
+    return _run_on(device, stream, call)
 
 
 def wq_topk_workspace_bytes(M: int, N: int, k: int) -> int:
