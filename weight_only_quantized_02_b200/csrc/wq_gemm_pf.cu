@@ -125,9 +125,22 @@ __device__ __forceinline__ uint32_t pf_map(const void *p, uint32_t rank)
 // Arrival on a barrier of either CTA.  What it hands over is in tensor memory,
 // ordered by tcgen05.fence; a release at cluster scope, which it does not need,
 // took 1400 cycles.
-__device__ __forceinline__ void pf_arrive(uint32_t cluster_bar)
+// One lane's (who) arrival for its warp, by predicate: the tensor-memory
+// instructions around it are the whole warp's, and a branch could leave the warp
+// split on the way to the next of them.
+__device__ __forceinline__ void pf_arrive(uint32_t cluster_bar, bool who)
 {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_bar),
+                 "r"((uint32_t)who)
+                 : "memory");
+}
+__device__ __forceinline__ void pf_arrive_own(uint64_t *bar, bool who) // a barrier of this CTA
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+                 "r"((uint32_t)who)
+                 : "memory");
 }
 // Barrier of the four warps of a retire group, and whether all of them are well.
 __device__ __forceinline__ bool pf_all(int id, bool ok)
@@ -396,8 +409,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
         if (i == chunks - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                pf_arrive(rt.ebar + b * 8);
+            pf_arrive(rt.ebar + b * 8, lane == 0);
         }
         if (whole) {
             if constexpr (BITS == 8)
@@ -414,8 +426,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
     }
     if (chunks == 0) { // few tokens: another group has them
         __syncwarp();
-        if (lane == 0)
-            pf_arrive(rt.ebar + b * 8);
+        pf_arrive(rt.ebar + b * 8, lane == 0);
     }
     if (whole)
         return;
@@ -714,14 +725,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                             pf_ffma2(tot[8 * (c + e) + j / 2], s2, v[e][j], v[e][j + 1]);
                 }
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sempty[ss]);
+                pf_arrive_own(&sempty[ss], lane == 0);
                 const bool end = ++kb == KB;
                 if (!end && g < nu - 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0)
-                        pf_arrive(rt.ebar + (g & 1) * 8);
+                    pf_arrive(rt.ebar + (g & 1) * 8, lane == 0);
                     continue;
                 }
                 // the tile's (or the run's) last group: the totals take its
@@ -819,8 +828,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                     fetch(1);
                 } else { // every value loaded from the weight stage has been used: release it
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&wempty[ws]);
+                    pf_arrive_own(&wempty[ws], lane == 0);
                     if (++ws == WS) {
                         ws = 0;
                         wpar ^= 1;
@@ -853,8 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
-                    pf_arrive(bar + (j % C::kAS) * 8);
+                pf_arrive(bar + (j % C::kAS) * 8, lane == 0);
             }
         }
     }
