@@ -495,6 +495,16 @@ int wq_gemv_i8_contributors(int bits, int K, int N, int G, int warps, int rb, in
  * caps its grid at the unit count). */
 int wq_stream_k_plan(long long U, int G, int KB, int *start, int *first, int *owner_table, int *owner_div);
 
+/* Debug view of how a prompt (more than 128 tokens, and fewer where a rule says
+ * so) with an epilogue is cut, on a GPU of `pairs` pairs of SMs and with a
+ * workspace of ws_bytes (0: none); group 0 or one that is stored as 128.  Host
+ * only, no GPU.  plan[5] = {tokens of an accumulator, accumulators of a tile,
+ * tiles of a pair of 128-channel panels, pairs of CTAs, 1: whole tiles a pair
+ * of CTAs, 0: equal runs of units, cutting tiles}.  WQ_ERR_NULL for a null
+ * plan, WQ_ERR_SHAPE for sizes out of range (or more units than 2^31, which
+ * the call itself runs in parts). */
+int wq_prompt_plan(int bits, int M, int K, int N, int pairs, size_t ws_bytes, int *plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -100,6 +100,7 @@ def _load():
         "wq_wait_selftest": (I, [I, P]),
         "wq_gemv_i8_plan": (I, [I, I, I, I, I, P, P]),
         "wq_gemv_i8_contributors": (I, [I, I, I, I, I, I, P, P, P]),
+        "wq_prompt_plan": (I, [I, I, I, I, I, SZ, P]),
         "wq_stream_k_plan": (I, [ctypes.c_longlong, I, I, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -621,6 +622,15 @@ def wq_gemv_i8_plan(bits: int, K: int, N: int, G: int, warps: int = 16):
     _check(lib.wq_gemv_i8_plan(bits, K, N, G, warps, meta, runs), "wq_gemv_i8_plan")
     return dict(CPR=meta[0], LB=meta[1], RB0=meta[2], RL=meta[3]), \
         [[tuple(runs[(c * warps + w) * 4:(c * warps + w) * 4 + 4]) for w in range(warps)] for c in range(G)]
+
+
+def wq_prompt_plan(bits: int, M: int, K: int, N: int, pairs: int = 74, ws_bytes: int = 0) -> dict:
+    """How a prompt with an epilogue is cut (host only): tokens of an
+    accumulator, accumulators of a tile, tiles of a pair of panels, pairs of
+    CTAs, whether they take whole tiles."""
+    plan = (ctypes.c_int * 5)()
+    _check(lib.wq_prompt_plan(bits, M, K, N, pairs, ws_bytes, plan), "wq_prompt_plan")
+    return dict(n=plan[0], nsub=plan[1], TT=plan[2], G=plan[3], align=bool(plan[4]))
 
 
 def wq_stream_k_plan(U: int, G: int, KB: int):

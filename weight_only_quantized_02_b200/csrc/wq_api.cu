@@ -321,6 +321,33 @@ int linear_prompt(const uint16_t *x, int M, int K, const void *Wq, const void *s
                   int group, int N, uint16_t *y, void *ws, size_t ws_bytes_given, cudaStream_t stream,
                   const EpiArgs &epi);
 
+// Whether a call with an epilogue and at most 128 tokens goes to the prompt
+// GEMM, without an entry of the dispatcher's table for it.  Measured on B200, us,
+// the layer's other kernels | the prompt GEMM:
+//   INT8, 5120 x 17408: M = 9 28 | 31, 16 41 | 31, 64 92 | 32, 128 51 | 35;
+//   17408 x 5120: M = 9 43 | 40, 64 178 | 48; 1024 x 1024: M = 9 16 | 12, 64 62 | 13;
+//   a 5120 x 152064 head: M = 9 138 | 222, 32 180 | 227, 64 367 | 259 (the integer
+//   kernels stream a large weight faster, but take long to begin);
+//   INT4, 5120 x 17408: M = 64 37 | 39, 96 50 | 41, 128 50 | 42; 17408 x 5120:
+//   M = 128 52 | 69; 4096 x 4096: 32 | 35; 1024 x 1024: M = 16 11 | 14, 128 26 | 16
+//   (the role-split GEMM cuts few panels more cheaply between the SMs).
+bool prompt_faster(int bits, int M, int K, int N)
+{
+    const long long codes = (long long)K * N;
+    if (bits == 8)
+        return M > 8 && (M > 10 || codes < (1LL << 26)) && (M > 32 || codes < (1LL << 28));
+    return M > 64 && (N > 120 * kPanelRows || codes <= (1LL << 23));
+}
+
+bool tuned(int M, int K, int N, int bits, int group)
+{
+    DeviceInfo d;
+    if (current_device_info(&d) != WQ_OK)
+        return false;
+    std::lock_guard<std::mutex> lk(g_mu);
+    return g_table.count(Key{device_key(d), M, K, N, bits, group}) != 0;
+}
+
 // The epilogue of the token rows from m0 on.
 EpiArgs epi_rows_from(const EpiArgs &e, int m0)
 {
@@ -346,7 +373,8 @@ int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *sca
     if (bits_of_group(group, &bits) != WQ_OK)
         return WQ_ERR_GROUP;
     const int chunk = chunk_tokens(bits, lgroup_of(bits, K, group));
-    if (epi && M > kChunkTokens && chunk == kChunkTokens && variant == WQ_VARIANT_AUTO)
+    if (epi && chunk == kChunkTokens && variant == WQ_VARIANT_AUTO &&
+        (M > kChunkTokens || (prompt_faster(bits, M, K, N) && !tuned(M, K, N, bits, group))))
         return linear_prompt(x, M, K, Wq, scales, zeros, bits, group, N, y, ws, ws_bytes_given, stream, *epi);
     if (M <= chunk)
         return linear_chunk(x, M, K, Wq, scales, zeros, group, N, y, variant, split, ws, ws_bytes_given, stream, epi);
@@ -388,20 +416,20 @@ int linear_prompt(const uint16_t *x, int M, int K, const void *Wq, const void *s
         return st;
     if (d.major != 10)
         return WQ_ERR_ARCH;
+    if (g_env_tuning != WQ_OK)
+        return g_env_tuning; // the table named by WQ_TUNING_FILE did not load
     void *w = ws;
     size_t have = ws_bytes_given;
     if (!w)
         registered_workspace(&w, &have);
     if (w && !aligned16(w))
         return WQ_ERR_ALIGN;
-    if (w && have < ws_bytes_gemm_pf())
-        w = nullptr; // whole tiles only
     const int most = pf_max_tokens(K, N);
     for (int m0 = 0; m0 < M; m0 += most) {
         const EpiArgs ec = epi_rows_from(epi, m0);
         LinearArgs a{x + (size_t)m0 * K, std::min(most, M - m0), K, N, Wq, scales, zeros, bits, bits == 8 ? 0 : 128,
                      y + (size_t)m0 * N * (epi.out_f32 ? 2 : 1), &ec};
-        if ((st = cuda_status(launch_gemm_pf(a, w, d.sm_count, stream))) != WQ_OK)
+        if ((st = cuda_status(launch_gemm_pf(a, w, have, d.sm_count, stream))) != WQ_OK)
             return st;
     }
     return WQ_OK;
@@ -1128,6 +1156,19 @@ int wq_wait_selftest(int limit_us, cudaStream_t stream)
     if (st != WQ_OK)
         return st;
     return cuda_status(launch_wait_selftest((uint64_t)limit_us * 1000u, stream));
+}
+
+int wq_prompt_plan(int bits, int M, int K, int N, int pairs, size_t ws_bytes_given, int *plan)
+{
+    if (!plan)
+        return WQ_ERR_NULL;
+    const int st = check_weight_shape(bits, K, N, bits == 8 ? 0 : 128);
+    if (st != WQ_OK)
+        return st;
+    if (M < 1 || M > kMaxTokens || pairs < 1)
+        return WQ_ERR_SHAPE;
+    pf_plan_debug(bits, M, K, N, pairs, ws_bytes_given, plan);
+    return plan[3] > 0 ? WQ_OK : WQ_ERR_SHAPE;
 }
 
 int wq_device_error(cudaStream_t stream)

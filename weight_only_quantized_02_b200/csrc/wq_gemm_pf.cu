@@ -43,6 +43,7 @@
 // the dequantization (2 units) and, for INT4, the retire warps (2 groups) that
 // the products are done.  Every wait is bounded (2 s); a timeout is recorded and
 // every role winds down.
+#include <atomic>
 #include <cstdint>
 
 #include "wq.h"
@@ -60,7 +61,6 @@ namespace {
 constexpr int kPfTok = 192;       // columns of an accumulator
 constexpr int kPfA0 = 2 * kPfTok; // first A column
 constexpr int kPfSS = 16;         // scale stages
-constexpr int kPfSplitUnits = 8;
 constexpr int kPfXB = kPfTok / 2 * 128;       // bytes of 64 k of an accumulator's tokens, one CTA's half
 constexpr int kPfOutB = 16 * kPanelRows * 4;  // 16 tokens of a CTA's channels on their way out, fp32
 static_assert(kPfA0 + 2 * 64 == 512, "tensor memory plan");
@@ -97,7 +97,7 @@ struct PfParams {
     const uint8_t *zeros;
     uint16_t *y;
     EpiArgs epi;
-    float *part;   // [pairs][2 slots][2 CTAs][kSub kPfTok tokens][128 rows]
+    float *part;   // [pairs][2 slots][2 CTAs][nsub n tokens][128 rows]
     uint32_t *cnt; // [pairs][2 CTAs][kGroups], by a split tile's first pair
 };
 
@@ -385,7 +385,6 @@ struct PfOut {
 template <int BITS>
 __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int tile, int b)
 {
-    constexpr int SUB = PfCfg<BITS>::kSub;
     const int KB = p.KB, lane = threadIdx.x & 31, nc = rt.nc, chunks = nc * p.nsub;
     const uint32_t tq = rt.tq + b * kPfTok;
     const bool whole = rt.u0 <= tile * KB && rt.u1 >= (tile + 1) * KB;
@@ -397,7 +396,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
     // pair c's partial of chunk i of this tile
     auto part_of = [&](int c, int i) {
         const int slot = pf_start(p, rt.G, c) / KB == tile ? 0 : 1, sub = i >= rt.nc ? 1 : 0;
-        return p.part + (((size_t)((c * 2 + slot) * 2 + rt.rank) * SUB + sub) * kPfTok +
+        return p.part + (((size_t)((c * 2 + slot) * 2 + rt.rank) * p.nsub + sub) * p.n +
                          16 * (rt.ch0 + i - sub * rt.nc)) * kPanelRows + out.r;
     };
     if (whole)
@@ -448,10 +447,11 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             t[j] = 0.f;
-        for (int cc = cf; cc <= cl; cc += 2) { // two contributors' loads in flight, added in order
-            float v[2][16];
+        constexpr int CG = 2; // contributors whose loads are in flight together, added in order
+        for (int cc = cf; cc <= cl; cc += CG) {
+            float v[CG][16];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < CG; ++e)
                 if (cc + e <= cl) {
                     const float *src = part_of(cc + e, i);
 #pragma unroll
@@ -459,7 +459,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
                         v[e][j] = __ldcg(src + j * kPanelRows);
                 }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < CG; ++e)
                 if (cc + e <= cl)
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -892,8 +892,64 @@ bool pf_x_map(CUtensorMap *map, const uint16_t *x, int M, int K, int rows)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How a launch is cut: tokens of an accumulator, accumulators and tiles, pairs of
+// CTAs, whole tiles or equal runs of units.
+struct PfPlan {
+    int n, nsub, TT, G, align;
+};
+
+// The cheapest of a few cuts, by times measured on B200 (us): a unit takes
+// 0.87 (INT4; its retirement, whatever the tokens) or 0.5 + 0.0018 a token
+// (INT8; dequantization, then the products), a tile 0.3 a 16-token chunk of its
+// two retire groups to write out, and cutting tiles between pairs 8 at once and 0.3 a
+// chunk for the partial sums and for each pair.  Many tokens a tile share a
+// dequantized block; more tiles keep all pairs busy without cutting them.
+PfPlan pf_plan(int bits, int M, int panels, int KB, int pairs, size_t ws_bytes)
+{
+    PfPlan best{0, 0, 0, 0, 1};
+    double best_us = 0;
+    const int pp = (panels + 1) / 2, sub = bits == 8 ? 2 : 1;
+    for (int nsub = 1; nsub <= (M <= kPfTok ? 1 : sub); ++nsub) {
+        for (int cut = 1; cut <= 6; ++cut) { // tiles of a channel panel pair: as few as hold the tokens, times cut
+            PfPlan q;
+            q.nsub = nsub;
+            const int least = (M + nsub * kPfTok - 1) / (nsub * kPfTok), most = (M + 16 * nsub - 1) / (16 * nsub);
+            const int want = least * cut < most ? least * cut : most;
+            q.n = ((M + want * nsub - 1) / (want * nsub) + 15) / 16 * 16;
+            q.TT = (M + nsub * q.n - 1) / (nsub * q.n);
+            const long long tiles = (long long)pp * q.TT, units = tiles * KB;
+            if (units >= (1LL << 31))
+                break;
+            const double tok = q.n * q.nsub, chunks = tok / 32;
+            const double unit = bits == 8 ? 0.5 + 0.0018 * tok : 0.87, out = 0.3 * chunks;
+            auto consider = [&](int G, int align, double us) {
+                if (best.G == 0 || us < best_us) {
+                    best_us = us;
+                    best = q;
+                    best.G = G;
+                    best.align = align;
+                }
+            };
+            const long long rounds = (tiles + pairs - 1) / pairs;
+            consider((int)(tiles < pairs ? tiles : pairs), 1, rounds * (KB * unit + out));
+            // equal runs: every pair, or a whole number of pairs a tile
+            for (int c = 2; c <= 8; ++c) {
+                const long long G = c == 8 ? pairs : tiles * c;
+                if (G > pairs || units < 4 * G) // a run of less than 512 k is not worth its partial sums
+                    continue;
+                if (ws_bytes < ws_counter_bytes() + (size_t)G * 4 * q.nsub * q.n * kPanelRows * sizeof(float))
+                    continue;
+                const double run = (double)units / G, parts = run >= KB ? 2 : KB / run + (c == 8 ? 1 : 0);
+                consider((int)G, 0,
+                         8 + run * unit + (run / KB + 1) * out + chunks * (0.3 + 0.3 * parts));
+            }
+        }
+    }
+    return best;
+}
+
 template <int BITS>
-cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+cudaError_t launch_pf_t(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st)
 {
     constexpr size_t smem = pf_smem_bytes<BITS>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
@@ -902,12 +958,14 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
         return e;
     // the warps' shares after setmaxnreg must fit what the CTA is launched with,
     // or the retire warps would wait for registers that never come
-    static int regs = 0; // the same on every device
+    static std::atomic<int> known{0}; // the same on every device
+    int regs = known.load(std::memory_order_relaxed);
     if (regs == 0) {
         cudaFuncAttributes fa;
         if ((e = cudaFuncGetAttributes(&fa, (const void *)gemm_pf_kernel<BITS>)) != cudaSuccess)
             return e;
         regs = fa.numRegs;
+        known.store(regs, std::memory_order_relaxed);
     }
     if (regs * PfCfg<BITS>::kThreads < PfCfg<BITS>::kRegs)
         return cudaErrorInvalidConfiguration;
@@ -917,16 +975,17 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
     p.N = a.N;
     p.KB = sh.kblocks();
     p.panels = sh.panels();
-    p.nsub = a.M <= kPfTok ? 1 : PfCfg<BITS>::kSub;
-    const int most_tok = p.nsub * kPfTok;
-    p.TT = (a.M + most_tok - 1) / most_tok;
-    p.n = ((a.M + p.TT * p.nsub - 1) / (p.TT * p.nsub) + 15) / 16 * 16;
-    p.TT = (a.M + p.nsub * p.n - 1) / (p.nsub * p.n);
-    const long long tiles = (long long)((p.panels + 1) / 2) * p.TT, units = tiles * p.KB;
-    if (units >= (1LL << 31))
+    const int pairs = sm_count / 2 < kPfMaxPairs ? sm_count / 2 : kPfMaxPairs;
+    const PfPlan plan = pf_plan(BITS, a.M, p.panels, p.KB, pairs, ws_bytes);
+    if (plan.G == 0)
         return cudaErrorInvalidValue; // the caller cuts M (pf_max_tokens)
-    p.tiles = (int)tiles;
-    p.U = (int)units;
+    p.nsub = plan.nsub;
+    p.n = plan.n;
+    p.TT = plan.TT;
+    p.tiles = (p.panels + 1) / 2 * p.TT;
+    p.U = p.tiles * p.KB;
+    p.align = plan.align;
+    const int G = plan.G;
     p.wq = (const uint8_t *)a.wq;
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
@@ -934,15 +993,6 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
     p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.part = ws ? (float *)((uint8_t *)ws + ws_counter_bytes()) : nullptr;
-    const int pairs = sm_count / 2 < kPfMaxPairs ? sm_count / 2 : kPfMaxPairs;
-    // Whole tiles a pair where the last round's idle pairs cost less than the
-    // split tiles' partial sums (about kPfSplitUnits units' time).
-    const long long rounds = (tiles + pairs - 1) / pairs;
-    p.align = !ws || rounds * p.KB <= units / pairs + kPfSplitUnits;
-    // at least four units a pair: a tile's sums are not cut finer than 512 k
-    const long long want = p.align ? tiles : (units + 3) / 4;
-    const long long parts = want > tiles ? want : tiles;
-    const int G = (int)(parts < pairs ? parts : pairs);
     CUtensorMap map;
     if (!pf_x_map(&map, a.x, a.M, a.K, p.n / 2))
         return cudaErrorInvalidValue;
@@ -961,7 +1011,14 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, int sm_count, cudaStream_
 
 } // namespace
 
-size_t ws_bytes_gemm_pf() { return ws_counter_bytes() + (size_t)kPfMaxPairs * 4 * PfCfg<8>::kSub * kPfTok * kPanelRows * sizeof(float); }
+void pf_plan_debug(int bits, int M, int K, int N, int pairs, size_t ws_bytes, int *plan)
+{
+    const PfPlan q = pf_plan(bits, M, (N + kPanelRows - 1) / kPanelRows, (K + kBlockK - 1) / kBlockK,
+                             pairs < kPfMaxPairs ? pairs : kPfMaxPairs, ws_bytes);
+    const int v[5] = {q.n, q.nsub, q.TT, q.G, q.align};
+    for (int i = 0; i < 5; ++i)
+        plan[i] = v[i];
+}
 
 // Tokens of one launch: its units stay below 2^31.
 int pf_max_tokens(int K, int N)
@@ -971,9 +1028,10 @@ int pf_max_tokens(int K, int N)
     return t > kMaxTokens ? kMaxTokens : (int)t;
 }
 
-cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st)
 {
-    return a.bits == 8 ? launch_pf_t<8>(a, ws, sm_count, st) : launch_pf_t<4>(a, ws, sm_count, st);
+    return a.bits == 8 ? launch_pf_t<8>(a, ws, ws ? ws_bytes : 0, sm_count, st)
+                       : launch_pf_t<4>(a, ws, ws ? ws_bytes : 0, sm_count, st);
 }
 
 cudaError_t read_gemm_pf_error(int *code, cudaStream_t st)

@@ -127,12 +127,13 @@ cudaError_t launch_gemm_i4(const LinearArgs &a, void *ws, int sm_count, cudaStre
 cudaError_t read_gemm_i4_error(int *code, cudaStream_t st);
 
 // Prompt GEMM on pairs of SMs (W8A16 and W4A16 of layout group 128), with an
-// epilogue (a.epi): any M up to pf_max_tokens; ws >= ws_bytes_gemm_pf(), or
-// NULL (no split tiles).
+// epilogue (a.epi): any M up to pf_max_tokens.  Tiles are cut between pairs
+// where the workspace (counters, then partial sums) holds their partial sums;
+// none is needed.
 constexpr int kPfMaxPairs = 80;
-size_t ws_bytes_gemm_pf();
 int pf_max_tokens(int K, int N);
-cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st);
+void pf_plan_debug(int bits, int M, int K, int N, int pairs, size_t ws_bytes, int *plan); // wq_prompt_plan
+cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st);
 cudaError_t read_gemm_pf_error(int *code, cudaStream_t st);
 
 // Integer GEMV (mma.sync m16n8k32 on the packed codes): M <= kGiMaxM,
