@@ -252,17 +252,21 @@ typedef struct {
  * only.  y may be the residual or mul buffer itself (same address, row stride
  * N: the residual stream updated in place); it must not overlap them, or x,
  * in any other way.
- *   epilogue  host, required; with every part absent the call is wq_linear
+ *   epilogue  host, required; with every part absent y is the layer, rounded
  *   ws        a workspace of ws_bytes for this call, as wq_linear_ex (zeroed by
  *             the caller before its first use; calls that share one must not
  *             overlap), or NULL: the registered one
- * Kernels, chunks and the workspace are the dispatcher's, as in wq_linear;
+ * Up to 128 tokens the kernel is the dispatcher's (a tuned entry, as in
+ * wq_linear), or the prompt GEMM where a rule on the sizes finds it faster; above
+ * 128 the prompt GEMM takes all tokens in one launch (INT4 groups stored as 128;
+ * other groups run 128 tokens at a time).  Neither fails for lack of workspace.
  * WQ_ERR_EPILOGUE for an unknown act or a row stride below N. */
 int wq_linear_epilogue(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
                        const void *zeros, int group, int N, const wq_epilogue *epilogue,
                        uint16_t *y, void *ws, size_t ws_bytes, cudaStream_t stream);
 
-/* wq_linear_f16 with an epilogue, its operands and y fp16.  No workspace. */
+/* wq_linear_f16 with an epilogue, its operands and y fp16.  No workspace; the
+ * row-block GEMV or the prompt GEMM on whole tiles, by a rule on the sizes. */
 int wq_linear_epilogue_f16(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
                            const void *zeros, int group, int N, const wq_epilogue *epilogue,
                            uint16_t *y, cudaStream_t stream);

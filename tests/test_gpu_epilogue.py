@@ -168,8 +168,8 @@ def test_int4_groups(bits, group, M):
     check(y, x, w, bias, "gelu", None, res, torch.bfloat16)
 
 
-@pytest.mark.parametrize("M", [1, 3, 32, 45])
-@pytest.mark.parametrize("bits,group", [(8, 0), (4, 32), (4, 64), (4, 128)])
+@pytest.mark.parametrize("M", [1, 3, 16, 17, 45, 150, 500])
+@pytest.mark.parametrize("bits,group", [(8, 0), (4, 32), (4, 64), (4, 128), (4, 640)])
 def test_f16(bits, group, M):
     K, N = 640, 336
     pw, w = make_weight(bits, group, K, N)
@@ -179,7 +179,7 @@ def test_f16(bits, group, M):
     check(y, x, w, bias, "gelu_tanh", mul, res, torch.float16)
 
 
-@pytest.mark.parametrize("M", [129, 200, 256, 300, 777])
+@pytest.mark.parametrize("M", [9, 11, 16, 33, 65, 128, 129, 200, 256, 300, 777])
 @pytest.mark.parametrize("bits,group,K,N", [(8, 0, 1056, 656), (8, 0, 96, 2064), (4, 128, 1024, 656), (4, 128, 256, 2064)])
 def test_prompts(bits, group, K, N, M):
     pw, w = make_weight(bits, group, K, N)
@@ -190,6 +190,44 @@ def test_prompts(bits, group, K, N, M):
     y = wq.wq_linear_epilogue(x, pw, bias=bias, act=wq.WQ_ACT_SILU, mul=mul, residual=res)
     check(y, x, w, bias, "silu", mul, res, torch.bfloat16)
     assert wq.wq_device_error() == 0
+
+
+@pytest.mark.parametrize("bits,group,K,N,M", [(8, 0, 4128, 528, 364), (8, 0, 8192, 144, 150), (4, 128, 4096, 528, 364),
+                                              (4, 128, 8192, 16, 400), (4, 128, 8192, 272, 70), (8, 0, 64, 3008, 385),
+                                              (8, 0, 6144, 16, 16), (4, 128, 128, 16, 193), (8, 0, 32, 16, 2000)])
+def test_prompts_of_few_panels(bits, group, K, N, M):
+    """Tiles cut between many pairs of CTAs, the parts summed by the last to
+    come; the same bits every time, from a workspace used over and over."""
+    pw, w = make_weight(bits, group, K, N)
+    x, bias, mul, res = operands(M, K, N, torch.bfloat16)
+    ws = ws_for(M, K, N)
+    first = None
+    for _ in range(3):
+        y = wq.wq_linear_epilogue(x, pw, bias=bias, act=wq.WQ_ACT_GELU, mul=mul, residual=res, ws=ws)
+        check(y, x, w, bias, "gelu", mul, res, torch.bfloat16)
+        first = y if first is None else first
+        assert torch.equal(y, first)
+    assert int(ws[:262912].max()) == 0
+    assert wq.wq_device_error() == 0
+
+
+@pytest.mark.parametrize("bits,group,M", [(8, 0, 200), (4, 128, 200), (8, 0, 40)])
+def test_prompt_workspace_edges(bits, group, M):
+    """A workspace too small for any partial sum, and canaries behind one that
+    holds them exactly."""
+    K, N = 4096, 400
+    pw, w = make_weight(bits, group, K, N)
+    x, bias, mul, res = operands(M, K, N, torch.bfloat16)
+    small = torch.zeros(262912, dtype=torch.uint8, device=dev())
+    y = wq.wq_linear_epilogue(x, pw, residual=res, ws=small)
+    check(y, x, w, None, "none", None, res, torch.bfloat16)
+    plan = wq.wq_prompt_plan(bits, M, K, N, torch.cuda.get_device_properties(0).multi_processor_count // 2, 1 << 30)
+    need = 262912 + plan["G"] * 4 * plan["nsub"] * plan["n"] * 128 * 4
+    buf = torch.zeros(need + 4096, dtype=torch.uint8, device=dev())
+    buf[need:] = 0xA5
+    y = wq.wq_linear_epilogue(x, pw, residual=res, ws=buf[:need])
+    check(y, x, w, None, "none", None, res, torch.bfloat16)
+    assert bool((buf[need:] == 0xA5).all())
 
 
 @pytest.mark.parametrize("M", [1, 4, 64, 150])

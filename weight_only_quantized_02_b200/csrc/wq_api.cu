@@ -339,6 +339,27 @@ bool prompt_faster(int bits, int M, int K, int N)
     return M > 64 && (N > 120 * kPanelRows || codes <= (1LL << 23));
 }
 
+// Whether an fp16 call with an epilogue goes to the prompt GEMM (whole tiles: that
+// entry has no workspace) or to the row-block GEMV's launches of 32 tokens, by the
+// times of both, us: a launch of the GEMV 4 and 0.25 a million weights up to 8 tokens,
+// 0.33 up to 16, above that 0.5 (INT8) or 0.7 (INT4); the prompt GEMM 5 and 0.61 or 0.8 for
+// each 128 of K in each round of its tiles over the pairs of SMs.  Measured on
+// B200, GEMV | prompt GEMM: INT8 5120 x 17408 M = 4 26 | 29, 9 32 | 29, 64 101 | 32;
+// 17408 x 5120 M = 24 56 | 83, 64 120 | 83, 150 312 | 86; 4096 x 4096 M = 16 8 | 23;
+// 1024 x 1024 M = 300 50 | 10; INT4 5120 x 17408 M = 16 35 | 39, 32 70 | 39, 64
+// 138 | 40; 17408 x 5120 M = 32 74 | 109, 150 367 | 112; 4096 x 4096 M = 64 36 | 32.
+bool f16_prompt_faster(int bits, int M, int K, int N, int sm_count)
+{
+    const int pairs = std::max(1, std::min(sm_count / 2, kPfMaxPairs));
+    const int tok = bits == 8 ? 384 : 192;
+    const long long tiles = (long long)((N + 2 * kPanelRows - 1) / (2 * kPanelRows)) * ((M + tok - 1) / tok);
+    const double rounds = (double)((tiles + pairs - 1) / pairs), blocks = (double)((K + kBlockK - 1) / kBlockK);
+    const double millions = (double)K * N * 1e-6, launch = 4 + millions * (bits == 8 ? 0.5 : 0.7);
+    const int rest = M % 32;
+    const double gemv = M / 32 * launch + (rest > 16 ? launch : rest ? 4 + (rest > 8 ? 0.33 : 0.25) * millions : 0);
+    return 5 + rounds * blocks * (bits == 8 ? 0.61 : 0.8) < gemv;
+}
+
 bool tuned(int M, int K, int N, int bits, int group)
 {
     DeviceInfo d;
@@ -690,6 +711,17 @@ static int linear_f16_impl(const uint16_t *x, int M, int K, const void *Wq, cons
     if (d.major != 10)
         return WQ_ERR_ARCH;
     const int lg = lgroup_of(bits, K, group), ks = default_rb_slices(K, N, d.sm_count);
+    if (epi && (bits == 8 || lg == 128) && f16_prompt_faster(bits, M, K, N, d.sm_count)) {
+        const int most = pf_max_tokens(K, N);
+        for (int m0 = 0; m0 < M; m0 += most) {
+            const EpiArgs ec = epi_rows_from(*epi, m0);
+            LinearArgs a{x + (size_t)m0 * K, std::min(most, M - m0), K, N, Wq, scales, zeros, bits,
+                         bits == 8 ? 0 : 128, y + (size_t)m0 * N, &ec};
+            if ((st = cuda_status(launch_gemm_pf(a, nullptr, 0, d.sm_count, stream, true))) != WQ_OK)
+                return st;
+        }
+        return WQ_OK;
+    }
     for (int m0 = 0; m0 < M; m0 += 32) { // the row-block GEMV: 32 tokens per launch
         const int mc = std::min(32, M - m0);
         EpiArgs ec;

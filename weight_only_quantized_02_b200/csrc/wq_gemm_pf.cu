@@ -208,15 +208,49 @@ __device__ __forceinline__ void pf_ffma2(unsigned long long &d, unsigned long lo
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(aa), "l"(bb));
 }
 
-// Two int8 codes (bytes lo, lo + 1 of w) as exact bf16: with the low seven
-// bits, 0x4300 | c is 128 + c; with the sign bit, 0x4300 | 0x80 is 256.
+// Exact integers in the activations' format.
+template <bool F16>
+__device__ __forceinline__ uint32_t pf_sub2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (F16)
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Two int8 codes (bytes 2 h, 2 h + 1 of w).  bf16: with the low seven bits,
+// 0x4300 | c is 128 + c; with the sign bit, 0x4300 | 0x80 is 256.  fp16: 0x6400 | c
+// is 1024 + c for the code plus 128 (its sign bit turned over).
+template <bool F16>
 __device__ __forceinline__ uint32_t pf_s8pair(uint32_t w, int h)
 {
+    if constexpr (F16)
+        return pf_sub2<true>(__byte_perm(w ^ 0x80808080u, 0x64646464u, h == 0 ? 0x4140u : 0x4342u), 0x64806480u);
     const uint32_t b = __byte_perm(w, 0u, h == 0 ? 0x4140u : 0x4342u);
     uint32_t mag, off;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(mag) : "r"(b), "r"(0x007F007Fu), "r"(0x43004300u));
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(off) : "r"(b), "r"(0x00800080u), "r"(0x43004300u));
-    return bf16x2_sub(mag, off);
+    return pf_sub2<false>(mag, off);
+}
+
+// One INT4 tile (16 rows x 64 k) as int4_tile_regs has it, in either format:
+// zlo, zhi are the format's {magic + z} pairs of this lane's two rows.
+template <bool F16>
+constexpr uint32_t kPfMagic2 = F16 ? 0x64006400u : 0x43004300u;
+template <bool F16>
+__device__ __forceinline__ void pf_int4_regs(const uint4 &w, uint32_t zlo, uint32_t zhi, uint32_t (&r)[16])
+{
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) // words x, y, z, w: rows lo, hi, lo, hi; registers 8 (i / 2) + 2 (i % 2) + ...
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t n;
+            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(n) : "r"(v[i] >> (4 * j)), "r"(0x000F000Fu), "r"(kPfMagic2<F16>));
+            r[8 * (i / 2) + 2 * (i % 2) + 4 * (j / 2) + j % 2] = pf_sub2<F16>(n, i % 2 ? zhi : zlo);
+        }
 }
 
 // First unit of pair c.
@@ -254,6 +288,7 @@ struct PfRetire {
 // take them out as 8 consecutive channels of a token a thread, so that y and
 // the operands move in 16-byte pieces, 256 contiguous bytes a token.  (Written
 // 2 bytes a lane, 64 a warp, a tile with a residual took 38 us to leave.)
+template <bool F16>
 struct PfOut {
     // copies: the launch parameters are behind a pointer here, and would be read
     // again after every barrier
@@ -285,7 +320,7 @@ struct PfOut {
         vec_res = ((reinterpret_cast<uintptr_t>(pres) | (uintptr_t)(2 * ld_res)) & 15) == 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            bias[j] = p.epi.bias && nn < N ? act16_to_float<false>(__ldg(p.epi.bias + nn + j)) : 0.f;
+            bias[j] = p.epi.bias && nn < N ? act16_to_float<F16>(__ldg(p.epi.bias + nn + j)) : 0.f;
     }
 
     // This thread's first token of chunk i (nc chunks of each accumulator in turn).
@@ -360,16 +395,21 @@ struct PfOut {
             for (int j = 0; j < 4; ++j) {
                 EpiOps lo{1.f, 0.f}, hi{1.f, 0.f};
                 if (pmul) {
-                    lo.mul = __uint_as_float(mw[j] << 16);
-                    hi.mul = __uint_as_float(mw[j] & 0xFFFF0000u);
+                    lo.mul = act16_to_float<F16>((uint16_t)mw[j]);
+                    hi.mul = act16_to_float<F16>((uint16_t)(mw[j] >> 16));
                 }
                 if (pres) {
-                    lo.res = __uint_as_float(rw[j] << 16);
-                    hi.res = __uint_as_float(rw[j] & 0xFFFF0000u);
+                    lo.res = act16_to_float<F16>((uint16_t)rw[j]);
+                    hi.res = act16_to_float<F16>((uint16_t)(rw[j] >> 16));
                 }
-                const __nv_bfloat162 q2 =
-                    __floats2bfloat162_rn(fmaf(x[2 * j], lo.mul, lo.res), fmaf(x[2 * j + 1], hi.mul, hi.res));
-                w[j] = *reinterpret_cast<const uint32_t *>(&q2);
+                const float y0 = fmaf(x[2 * j], lo.mul, lo.res), y1 = fmaf(x[2 * j + 1], hi.mul, hi.res);
+                if constexpr (F16) {
+                    const __half2 q2 = __floats2half2_rn(y0, y1);
+                    w[j] = *reinterpret_cast<const uint32_t *>(&q2);
+                } else {
+                    const __nv_bfloat162 q2 = __floats2bfloat162_rn(y0, y1);
+                    w[j] = *reinterpret_cast<const uint32_t *>(&q2);
+                }
             }
             *reinterpret_cast<uint4 *>(y + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -382,13 +422,13 @@ struct PfOut {
 // accumulators are released after the last column is read.  Called by the four
 // warps of a group together.  Out of line, so that the retire loop keeps its
 // registers.
-template <int BITS>
+template <int BITS, bool F16>
 __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int tile, int b)
 {
     const int KB = p.KB, lane = threadIdx.x & 31, nc = rt.nc, chunks = nc * p.nsub;
     const uint32_t tq = rt.tq + b * kPfTok;
     const bool whole = rt.u0 <= tile * KB && rt.u1 >= (tile + 1) * KB;
-    PfOut out(p, rt, tile);
+    PfOut<F16> out(p, rt, tile);
     float scale = 1.f;
     const int row = out.nn - out.og + out.r; // the channel whose sums this thread holds
     if (BITS == 8 && row < out.N)
@@ -475,7 +515,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
         atomicExch(counter, 0u); // ready for the next call
 }
 
-template <int BITS>
+template <int BITS, bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThreads, 1)
     gemm_pf_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ PfParams p)
 {
@@ -615,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
             // whose slots, stages and parities are then constants: the loop's own
             // instructions cost as much as the products otherwise.
             const bool issuer = pf_elect();
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.n >> 3) << 17) | (16u << 24);
+            const uint32_t idesc = (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(p.n >> 3) << 17) | (16u << 24);
             const uint64_t bdesc0 = smem_desc_sw128(smem_u32(sX));
             int kb = kb0, tiles = 0; // tiles begun (INT8)
             uint32_t par = 0;        // of this round of the x ring
@@ -749,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                 tmem_wait_st();
                 ok = pf_all(1 + h, ok);
                 if (ok)
-                    pf_flush<BITS>(p, rt, tile, g & 1);
+                    pf_flush<BITS, F16>(p, rt, tile, g & 1);
 #pragma unroll
                 for (int j = 0; j < C::kChunks * 8; ++j)
                     tot[j] = 0ull;
@@ -763,7 +803,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                 if (!ok)
                     break; // the whole group
                 tc_fence_after();
-                pf_flush<BITS>(p, rt, tile, 0);
+                pf_flush<BITS, F16>(p, rt, tile, 0);
             }
         }
     } else {
@@ -792,8 +832,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
             if (BITS == 4 && h0 == 0) { // rows 16 blkrow + g and + 8
                 const uint8_t *zp = sZ + ws * 128 + 8 * blkrow + (g >> 1);
                 const uint32_t z0 = (zp[0] >> (4 * (g & 1))) & 0xFu, z1 = (zp[4] >> (4 * (g & 1))) & 0xFu;
-                zlo = 0x43004300u | z0 | (z0 << 16);
-                zhi = 0x43004300u | z1 | (z1 << 16);
+                zlo = kPfMagic2<F16> | z0 | (z0 << 16);
+                zhi = kPfMagic2<F16> | z1 | (z1 << 16);
             }
         };
         ok = mbar_wait_warp(&wfull[0], 0);
@@ -812,14 +852,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
 #pragma unroll
                 for (int hf = 0; hf < AH; ++hf) {
                     if constexpr (BITS == 4) {
-                        int4_tile_regs(w[hf], zlo, zhi, rr[hf]);
+                        pf_int4_regs<F16>(w[hf], zlo, zhi, rr[hf]);
                     } else {
                         const uint4 a = w[2 * hf], b = w[2 * hf + 1];
                         const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            rr[hf][2 * i] = pf_s8pair(v[i], 0);
-                            rr[hf][2 * i + 1] = pf_s8pair(v[i], 1);
+                            rr[hf][2 * i] = pf_s8pair<F16>(v[i], 0);
+                            rr[hf][2 * i + 1] = pf_s8pair<F16>(v[i], 1);
                         }
                     }
                 }
@@ -948,12 +988,12 @@ PfPlan pf_plan(int bits, int M, int panels, int KB, int pairs, size_t ws_bytes)
     return best;
 }
 
-template <int BITS>
+template <int BITS, bool F16>
 cudaError_t launch_pf_t(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st)
 {
     constexpr size_t smem = pf_smem_bytes<BITS>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
-    cudaError_t e = kernel_setup((const void *)gemm_pf_kernel<BITS>, smem, 0, 0, nullptr);
+    cudaError_t e = kernel_setup((const void *)gemm_pf_kernel<BITS, F16>, smem, 0, 0, nullptr);
     if (e != cudaSuccess)
         return e;
     // the warps' shares after setmaxnreg must fit what the CTA is launched with,
@@ -962,7 +1002,7 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_c
     int regs = known.load(std::memory_order_relaxed);
     if (regs == 0) {
         cudaFuncAttributes fa;
-        if ((e = cudaFuncGetAttributes(&fa, (const void *)gemm_pf_kernel<BITS>)) != cudaSuccess)
+        if ((e = cudaFuncGetAttributes(&fa, (const void *)gemm_pf_kernel<BITS, F16>)) != cudaSuccess)
             return e;
         regs = fa.numRegs;
         known.store(regs, std::memory_order_relaxed);
@@ -1006,7 +1046,7 @@ cudaError_t launch_pf_t(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_c
     cfg.blockDim = dim3(PfCfg<BITS>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, gemm_pf_kernel<BITS>, map, p);
+    return cudaLaunchKernelEx(&cfg, gemm_pf_kernel<BITS, F16>, map, p);
 }
 
 } // namespace
@@ -1028,10 +1068,14 @@ int pf_max_tokens(int K, int N)
     return t > kMaxTokens ? kMaxTokens : (int)t;
 }
 
-cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st)
+cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st, bool f16)
 {
-    return a.bits == 8 ? launch_pf_t<8>(a, ws, ws ? ws_bytes : 0, sm_count, st)
-                       : launch_pf_t<4>(a, ws, ws ? ws_bytes : 0, sm_count, st);
+    const size_t have = ws ? ws_bytes : 0;
+    if (f16)
+        return a.bits == 8 ? launch_pf_t<8, true>(a, ws, have, sm_count, st)
+                           : launch_pf_t<4, true>(a, ws, have, sm_count, st);
+    return a.bits == 8 ? launch_pf_t<8, false>(a, ws, have, sm_count, st)
+                       : launch_pf_t<4, false>(a, ws, have, sm_count, st);
 }
 
 cudaError_t read_gemm_pf_error(int *code, cudaStream_t st)

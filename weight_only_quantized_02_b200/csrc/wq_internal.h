@@ -133,7 +133,8 @@ cudaError_t read_gemm_i4_error(int *code, cudaStream_t st);
 constexpr int kPfMaxPairs = 80;
 int pf_max_tokens(int K, int N);
 void pf_plan_debug(int bits, int M, int K, int N, int pairs, size_t ws_bytes, int *plan); // wq_prompt_plan
-cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st);
+cudaError_t launch_gemm_pf(const LinearArgs &a, void *ws, size_t ws_bytes, int sm_count, cudaStream_t st,
+                           bool f16 = false); // f16: fp16 activations, operands and outputs instead of bf16
 cudaError_t read_gemm_pf_error(int *code, cudaStream_t st);
 
 // Integer GEMV (mma.sync m16n8k32 on the packed codes): M <= kGiMaxM,
