@@ -105,10 +105,7 @@ __device__ __forceinline__ void gemm_store(const GemmParams &p, int panel, int s
 #pragma unroll
             for (int m0 = 0; m0 < NT; m0 += 16) {
                 EpiOps o[16]; // a batch's operands in flight together
-#pragma unroll
-                for (int m = 0; m < 16; ++m)
-                    if (m0 + m < p.M)
-                        o[m] = epi_load<EPI>(p.epi, m0 + m, n);
+                epi_load_tokens<EPI>(p.epi, o, m0, p.M - m0, n);
 #pragma unroll
                 for (int m = 0; m < 16; ++m)
                     if (m0 + m < p.M)

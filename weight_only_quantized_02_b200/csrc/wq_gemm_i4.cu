@@ -130,12 +130,9 @@ __device__ __forceinline__ void umma_ts_i8(uint32_t d_tmem, uint32_t a_tmem, uin
 template <bool EPI, int MM>
 __device__ __forceinline__ float i4_epi_ops(const I4Params &p, int n, int M, EpiOps (&ops)[MM])
 {
+    epi_load_tokens<EPI>(p.epi, ops, 0, n < p.N ? M : 0, n);
     if (n >= p.N)
         return 0.f;
-#pragma unroll
-    for (int m = 0; m < MM; ++m)
-        if (m < M)
-            ops[m] = epi_load<EPI>(p.epi, m, n);
     return epi_bias<EPI>(p.epi, n);
 }
 

@@ -110,12 +110,9 @@ constexpr size_t i8_smem_bytes()
 template <bool EPI, int CNT>
 __device__ __forceinline__ float i8_epi_ops(const I8Params &p, int n, int m0, int M, EpiOps (&ops)[CNT])
 {
+    epi_load_tokens<EPI>(p.epi, ops, m0, n < p.N ? M - m0 : 0, n);
     if (n >= p.N)
         return 0.f;
-#pragma unroll
-    for (int t = 0; t < CNT; ++t)
-        if (m0 + t < M)
-            ops[t] = epi_load<EPI>(p.epi, m0 + t, n);
     return epi_bias<EPI>(p.epi, n);
 }
 

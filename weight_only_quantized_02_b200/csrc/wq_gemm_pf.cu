@@ -393,16 +393,16 @@ struct PfOut {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                EpiOps lo{1.f, 0.f}, hi{1.f, 0.f};
+                float m0 = 1.f, m1 = 1.f, r0 = 0.f, r1 = 0.f;
                 if (pmul) {
-                    lo.mul = act16_to_float<F16>((uint16_t)mw[j]);
-                    hi.mul = act16_to_float<F16>((uint16_t)(mw[j] >> 16));
+                    m0 = act16_to_float<F16>((uint16_t)mw[j]);
+                    m1 = act16_to_float<F16>((uint16_t)(mw[j] >> 16));
                 }
                 if (pres) {
-                    lo.res = act16_to_float<F16>((uint16_t)rw[j]);
-                    hi.res = act16_to_float<F16>((uint16_t)(rw[j] >> 16));
+                    r0 = act16_to_float<F16>((uint16_t)rw[j]);
+                    r1 = act16_to_float<F16>((uint16_t)(rw[j] >> 16));
                 }
-                const float y0 = fmaf(x[2 * j], lo.mul, lo.res), y1 = fmaf(x[2 * j + 1], hi.mul, hi.res);
+                const float y0 = fmaf(x[2 * j], m0, r0), y1 = fmaf(x[2 * j + 1], m1, r1);
                 if constexpr (F16) {
                     const __half2 q2 = __floats2half2_rn(y0, y1);
                     w[j] = *reinterpret_cast<const uint32_t *>(&q2);

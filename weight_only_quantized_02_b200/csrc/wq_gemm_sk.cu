@@ -269,10 +269,7 @@ __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kM
 #pragma unroll
                     for (int c0 = 0; c0 < HALF; c0 += B) {
                         EpiOps o[B];
-#pragma unroll
-                        for (int c = 0; c < B; ++c)
-                            if (h * HALF + c0 + c < p.M)
-                                o[c] = epi_load<EPI>(p.epi, h * HALF + c0 + c, nrow);
+                        epi_load_tokens<EPI>(p.epi, o, h * HALF + c0, p.M - h * HALF - c0, nrow);
 #pragma unroll
                         for (int c = 0; c < B; ++c)
                             if (h * HALF + c0 + c < p.M)
@@ -336,10 +333,7 @@ __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kM
                 if (nrow < p.N) {
                     const float bias = epi_bias<EPI>(p.epi, nrow);
                     EpiOps o[CH];
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        if (h * HALF + c0 + c < p.M)
-                            o[c] = epi_load<EPI>(p.epi, h * HALF + c0 + c, nrow);
+                    epi_load_tokens<EPI>(p.epi, o, h * HALF + c0, p.M - h * HALF - c0, nrow);
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
                         if (h * HALF + c0 + c < p.M)

@@ -144,16 +144,23 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
                                          int t0, bool whole = false)
 {
     const int nrow = pnl * kPanelRows + r;
-    // fewer in flight beside an epilogue's operands from 64 tokens on, whose totals
-    // would spill otherwise (64 tokens: 50 us without any operand; the plain layer 33)
-    constexpr int CG = EPI && NT >= 64 ? 2 : 4, EB = NT >= 64 ? 8 : 16;
-    for (int j0 = 0; j0 < CW; j0 += 16) {
-        float acc[16];
+    // With an epilogue 8 tokens at a time, the operands' loads beside the partials':
+    // 16, and the operands behind the sums, were twice the trips to L2 and would
+    // spill at 64 tokens.
+    constexpr int CG = 4, TB = EPI ? 8 : 16;
+    float bias = 0.f;
+    if (nrow < p.N)
+        bias = epi_bias<EPI>(p.epi, nrow);
+    for (int j0 = 0; j0 < CW; j0 += TB) {
+        const int jn = min(TB, p.M - t0 - j0);
+        float acc[TB];
+        EpiOps o[TB];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < TB; ++j)
             acc[j] = 0.f;
+        epi_load_tokens<EPI>(p.epi, o, t0 + j0, nrow < p.N ? jn : 0, nrow);
         for (int c0 = cf; c0 <= cl; c0 += CG) {
-            float v[CG][16];
+            float v[CG][TB];
 #pragma unroll
             for (int u = 0; u < CG; ++u) {
                 const int cc = c0 + u;
@@ -161,7 +168,7 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
                     const int sl = pnl == sk.first[cc] && !whole ? 0 : 1;
                     const float *src = p.part + ((size_t)(cc * 2 + sl) * NT + t0 + j0) * kPanelRows + r;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < TB; ++j)
                         v[u][j] = __ldcg(src + j * kPanelRows);
                 }
             }
@@ -169,12 +176,22 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
             for (int u = 0; u < CG; ++u) // in CTA order
                 if (c0 + u <= cl)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < TB; ++j)
                         acc[j] += v[u][j];
         }
+        EpiArgs rest = p.epi;
+        if (EPI && !p.epi.out_f32) {
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+                acc[j] += bias;
+            epi_activations(acc, p.epi.act);
+            rest.act = WQ_ACT_NONE;
+        }
         if (nrow < p.N) {
-            const int jn = min(16, p.M - t0 - j0);
-            epi_store_tokens<EPI, 16, EB>(p.epi, p.y, p.N, t0 + j0, jn, nrow, acc);
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+                if (j < jn)
+                    epi_store<EPI>(rest, p.y, p.N, t0 + j0 + j, nrow, acc[j], 0.f, o[j]);
         }
     }
 }

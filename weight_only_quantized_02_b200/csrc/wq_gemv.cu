@@ -400,25 +400,20 @@ __global__ void __launch_bounds__(kGemvWarps * 32) gemv_kernel(const GemvParams 
                 s_hi = bf16_bits_to_float(__ldg(p.scales + n_hi));
             }
             const float b_lo = epi_bias<EPI, F16>(p.epi, n_lo), b_hi = epi_bias<EPI, F16>(p.epi, n_hi);
-            EpiOps o_lo[MT][2], o_hi[MT][2]; // every operand in flight together
+            EpiOps o[4 * MT]; // every operand in flight together
+            epi_load_batch<EPI, F16>(p.epi, o, [&](int j, int &m, int &n) {
+                m = 8 * (j / 4) + 2 * t + j / 2 % 2;
+                n = j % 2 ? n_hi : n_lo;
+                return m < p.M;
+            });
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int m = 8 * mt + 2 * t + e;
                     if (m < p.M) {
-                        o_lo[mt][e] = epi_load<EPI, F16>(p.epi, m, n_lo);
-                        o_hi[mt][e] = epi_load<EPI, F16>(p.epi, m, n_hi);
-                    }
-                }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int m = 8 * mt + 2 * t + e;
-                    if (m < p.M) {
-                        epi_store<EPI, F16>(p.epi, p.y, p.N, m, n_lo, acc[mt][e] * s_lo, b_lo, o_lo[mt][e]);
-                        epi_store<EPI, F16>(p.epi, p.y, p.N, m, n_hi, acc[mt][2 + e] * s_hi, b_hi, o_hi[mt][e]);
+                        epi_store<EPI, F16>(p.epi, p.y, p.N, m, n_lo, acc[mt][e] * s_lo, b_lo, o[4 * mt + 2 * e]);
+                        epi_store<EPI, F16>(p.epi, p.y, p.N, m, n_hi, acc[mt][2 + e] * s_hi, b_hi, o[4 * mt + 2 * e + 1]);
                     }
                 }
         }

@@ -324,7 +324,7 @@ __device__ __forceinline__ void gi_emit(const GiParams &p, int n0, const int *s_
         const int q = q0 + lane, r = q & 15, m = q >> 4;
         bool redo = false;
         float bias = 0.f;
-        EpiOps o{1.f, 0.f};
+        EpiOps o = epi_none();
         if (q < 16 * M) {
             o = epi_load<EPI>(p.epi, m, n0 + r);
             bias = epi_bias<EPI>(p.epi, n0 + r);

@@ -249,7 +249,12 @@ __global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const GemvSkPa
             auto store_y = [&](const float (&v)[MT][4]) {
                 const float b_lo = n_lo < p.N ? epi_bias<EPI>(p.epi, n_lo) : 0.f;
                 const float b_hi = n_hi < p.N ? epi_bias<EPI>(p.epi, n_hi) : 0.f;
-                EpiOps o_lo[MT][2], o_hi[MT][2]; // every operand in flight together
+                EpiOps o[4 * MT]; // every operand in flight together
+                epi_load_batch<EPI>(p.epi, o, [&](int j, int &m, int &n) {
+                    m = 8 * (j / 4) + 2 * t + j / 2 % 2;
+                    n = j % 2 ? n_hi : n_lo;
+                    return m < p.M && n < p.N;
+                });
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -257,21 +262,9 @@ __global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const GemvSkPa
                         const int m = 8 * mt + 2 * t + e;
                         if (m < p.M) {
                             if (n_lo < p.N)
-                                o_lo[mt][e] = epi_load<EPI>(p.epi, m, n_lo);
+                                epi_store<EPI>(p.epi, p.y, p.N, m, n_lo, v[mt][e] * s_lo, b_lo, o[4 * mt + 2 * e]);
                             if (n_hi < p.N)
-                                o_hi[mt][e] = epi_load<EPI>(p.epi, m, n_hi);
-                        }
-                    }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int m = 8 * mt + 2 * t + e;
-                        if (m < p.M) {
-                            if (n_lo < p.N)
-                                epi_store<EPI>(p.epi, p.y, p.N, m, n_lo, v[mt][e] * s_lo, b_lo, o_lo[mt][e]);
-                            if (n_hi < p.N)
-                                epi_store<EPI>(p.epi, p.y, p.N, m, n_hi, v[mt][2 + e] * s_hi, b_hi, o_hi[mt][e]);
+                                epi_store<EPI>(p.epi, p.y, p.N, m, n_hi, v[mt][2 + e] * s_hi, b_hi, o[4 * mt + 2 * e + 1]);
                         }
                     }
             };
