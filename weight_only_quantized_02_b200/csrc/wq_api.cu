@@ -328,15 +328,18 @@ int linear_prompt(const uint16_t *x, int M, int K, const void *Wq, const void *s
 //   17408 x 5120: M = 9 43 | 40, 64 178 | 48; 1024 x 1024: M = 9 16 | 12, 64 62 | 13;
 //   a 5120 x 152064 head: M = 9 138 | 222, 32 180 | 227, 64 367 | 259 (the integer
 //   kernels stream a large weight faster, but take long to begin);
-//   INT4, 5120 x 17408: M = 64 37 | 39, 96 50 | 41, 128 50 | 42; 17408 x 5120:
-//   M = 128 52 | 69; 4096 x 4096: 32 | 35; 1024 x 1024: M = 16 11 | 14, 128 26 | 16
-//   (the role-split GEMM cuts few panels more cheaply between the SMs).
+//   INT4, 5120 x 17408: M = 64 37 | 41, 96 53 | 43, 128 53 | 43; 17408 x 5120:
+//   M = 96 53 | 64; 4096 x 4096: M = 128 32 | 35; 5120 x 5120: M = 100 34 | 47;
+//   2048 x 8192: M = 100 28 | 21; 2048 x 4096: M = 64 20 | 20, 66 33 | 20;
+//   1024 x 1024: M = 32 13 | 12, 64 15 | 12, 128 24 | 12; 4096 x 1024: M = 40 24 | 20,
+//   100 37 | 25; 1024 x 5120: M = 64 22 | 13 (above 64 tokens the role-split GEMM's
+//   retirement is slower a block, but it cuts long K more cheaply between the SMs).
 bool prompt_faster(int bits, int M, int K, int N)
 {
     const long long codes = (long long)K * N;
     if (bits == 8)
         return M > 8 && (M > 10 || codes < (1LL << 26)) && (M > 32 || codes < (1LL << 28));
-    return M > 64 && (N > 120 * kPanelRows || codes <= (1LL << 23));
+    return (M > 32 && codes <= (1LL << 23)) || (M > 64 && (N > 120 * kPanelRows || K <= 2048));
 }
 
 // Whether an fp16 call with an epilogue goes to the prompt GEMM (whole tiles: that
