@@ -31,18 +31,29 @@
 // the partial sums of a tile that two or more pairs share are added in their
 // order by the last to arrive), or whole tiles where there is no workspace.
 //
-// Warps (INT4 24, INT8 20; registers are moved to the roles that need them):
+// Warps (20; registers are moved to the roles that need them):
 //   0      x producer: the CTA's half of the tile's tokens, 64 k a stage (tensor
 //          map, 128-byte swizzle), signalled on the leader's barrier
-//   1      weight producer: a unit's packed block (and zero points, scales)
+//   1      weight producer: a unit's packed block (and zero points)
 //   2      tensor memory; in the leader CTA, the lane that issues the MMAs
-//   4-15   (INT8: 4-11) retire warps: lane quadrant x a third (half) of the
-//          token columns
-//   the last eight   dequantization: packed block -> exact integers in tensor memory
+//   4-11   retire warps: lane quadrant x half of the token columns; INT4 scales go
+//          from global memory to a register two groups ahead (through shared
+//          memory and a barrier of their own they took 280 cycles a group)
+//   12-19  dequantization: packed block -> exact integers in tensor memory
 // One commit for each 64 k, to both CTAs, tells the x producers (8 or 4 stages),
 // the dequantization (2 units) and, for INT4, the retire warps (2 groups) that
-// the products are done.  Every wait is bounded (2 s); a timeout is recorded and
-// every role winds down.
+// the products are done.
+//
+// Measured on B200 (layer with a residual or the other half of a gate, the weights
+// in L2): INT4 17408 x 5120, 2048 tokens 357 us (1020 TFLOP/s); 5120 x 17408, 364
+// tokens 82; INT8 17408 x 5120, 2048 tokens 314 (1170 TFLOP/s; the tensor pipe busy
+// in 98 % of the cycles, at a clock that the power limit holds at 1.0 to 1.4 GHz);
+// 5120 x 17408, 333 tokens 58.  INT4 is held by the work beside the products: a unit
+// takes some 1350 cycles against 768 of products at 192 tokens, the dequantization
+// about 1200 of its warps' time and the retirement 900, both by instruction
+// latency at one or two warps a scheduler.
+//
+// Every wait is bounded (2 s); a timeout is recorded and every role winds down.
 #include <atomic>
 #include <cstdint>
 
@@ -60,7 +71,6 @@ namespace {
 
 constexpr int kPfTok = 192;       // columns of an accumulator
 constexpr int kPfA0 = 2 * kPfTok; // first A column
-constexpr int kPfSS = 16;         // scale stages
 constexpr int kPfXB = kPfTok / 2 * 128;       // bytes of 64 k of an accumulator's tokens, one CTA's half
 constexpr int kPfOutB = 16 * kPanelRows * 4;  // 16 tokens of a CTA's channels on their way out, fp32
 static_assert(kPfA0 + 2 * 64 == 512, "tensor memory plan");
@@ -82,8 +92,8 @@ struct PfCfg {
     static constexpr int kThreads = 128 + kGroups * 128 + 256;
     // registers a thread at launch, and by role
     static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
-    static constexpr int kRegsIssue = 32, kRegsRetire = BITS == 4 ? 168 : 144,
-                         kRegsDequant = BITS == 4 ? 56 : 80;
+    static constexpr int kRegsIssue = 32, kRegsRetire = BITS == 4 ? 176 : 144,
+                         kRegsDequant = BITS == 4 ? 48 : 80;
     static constexpr int kRegs = 128 * kRegsIssue + kGroups * 128 * kRegsRetire + 256 * kRegsDequant;
     static_assert(kRegs <= kThreads * kRegsLaunch, "the roles' registers come out of the CTA's at launch");
     static_assert(kUnroll % 2 == 0, "a unit's A stage and accumulator are constants of the unrolled loops");
@@ -105,8 +115,8 @@ template <int BITS>
 constexpr size_t pf_smem_bytes()
 {
     using C = PfCfg<BITS>;
-    return 1024 + (size_t)C::kXS * C::kXB + (size_t)C::kWS * C::kWB + 2 * C::kGroups * kPfOutB + (size_t)kPfSS * 256 +
-           (size_t)C::kWS * 128 + (size_t)(2 * C::kXS + 2 * C::kWS + 2 * kPfSS + C::kAS + 4) * 8 + 32;
+    return 1024 + (size_t)C::kXS * C::kXB + (size_t)C::kWS * C::kWB + 2 * C::kGroups * kPfOutB +
+           (size_t)C::kWS * 128 + (size_t)(2 * C::kXS + 2 * C::kWS + C::kAS + 4) * 8 + 32;
 }
 
 // ---- pairs of CTAs ----
@@ -357,6 +367,16 @@ struct PfOut {
     // before; fetches the next chunk's, if there is one.
     __device__ __forceinline__ void emit(int i, bool next, const float (&v)[16])
     {
+        if (out_f32) { // a warp's 32 channels are 128 bytes of a token already
+            float *yp = reinterpret_cast<float *>(y);
+            const int m0 = token(i) - ot, row = nn - og + r;
+            if (row < N)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (m0 + j < M)
+                        yp[(size_t)(m0 + j) * N + row] = v[j];
+            return;
+        }
         float *buf = obuf + ob * (kPfOutB / 4);
         ob ^= 1; // a buffer is written again after the other one's barrier: its readers are through
 #pragma unroll
@@ -377,12 +397,6 @@ struct PfOut {
             const float4 a = *reinterpret_cast<const float4 *>(buf + (ot + 8 * e) * kPanelRows + og);
             const float4 b = *reinterpret_cast<const float4 *>(buf + (ot + 8 * e) * kPanelRows + og + 4);
             const size_t at = (size_t)m * N + nn;
-            if (out_f32) {
-                float4 *yp = reinterpret_cast<float4 *>(reinterpret_cast<float *>(y) + at);
-                yp[0] = a;
-                yp[1] = b;
-                continue;
-            }
             float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -526,14 +540,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
     uint8_t *sX = smem;                 // XS x stages, 1024-byte aligned
     uint8_t *sW = sX + XS * XB;         // WS packed blocks
     uint8_t *sO = sW + (size_t)WS * WB;           // two output buffers for each retire group
-    uint8_t *sS = sO + 2 * C::kGroups * kPfOutB; // kPfSS group scales
-    uint8_t *sZ = sS + kPfSS * 256;    // WS zero points
+    uint8_t *sZ = sO + 2 * C::kGroups * kPfOutB;  // WS zero points
     uint64_t *xfull = reinterpret_cast<uint64_t *>(sZ + WS * 128);
     uint64_t *done = xfull + XS;
     uint64_t *afull = done + XS;
     uint64_t *wfull = afull + C::kAS, *wempty = wfull + WS;
-    uint64_t *sfull = wempty + WS, *sempty = sfull + kPfSS;
-    uint64_t *accfull = sempty + kPfSS, *accempty = accfull + 2;
+    uint64_t *accfull = wempty + WS, *accempty = accfull + 2;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(accempty + 2);
     uint32_t *s_ticket = s_tmem + 1; // [kGroups]
 
@@ -552,10 +564,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
         for (int s = 0; s < WS; ++s) {
             mbar_init(&wfull[s], 1);
             mbar_init(&wempty[s], 8);
-        }
-        for (int s = 0; s < kPfSS; ++s) {
-            mbar_init(&sfull[s], 1);
-            mbar_init(&sempty[s], 4 * C::kGroups);
         }
         for (int s = 0; s < C::kAS; ++s)
             mbar_init(&afull[s], 16); // the dequantization warps of both CTAs
@@ -622,19 +630,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                         bulk_g2s(sZ + ws * 128, p.zeros + blk * 64, 64, &wfull[ws], pol);
                 } else {
                     mbar_arrive(&wfull[ws]); // no such panel: its rows are never written
-                }
-                if constexpr (BITS == 4) {
-                    const int ss = i % kPfSS;
-                    if (i >= kPfSS && !mbar_wait(&sempty[ss], ((i / kPfSS) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (pnl < p.panels) {
-                        mbar_arrive_expect_tx(&sfull[ss], 256);
-                        bulk_g2s(sS + ss * 256, p.scales + blk * kPanelRows, 256, &sfull[ss], pol);
-                    } else {
-                        mbar_arrive(&sfull[ss]);
-                    }
                 }
                 if (++ws == WS) {
                     ws = 0;
@@ -741,14 +736,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
             for (int j = 0; j < C::kChunks * 8; ++j)
                 tot[j] = 0ull;
             int tile = tile0, kb = kb0;
+            // this thread's scales, two groups ahead of their use within a tile
+            const uint16_t *sp;
+            uint16_t sc0, sc1;
+            auto scales_of = [&]() { // of (tile, kb) and the group after it
+                const int pnl = min(2 * (tile / p.TT) + (int)rank, p.panels - 1); // a panel past the last is never written
+                sp = p.scales + ((size_t)pnl * KB + kb) * kPanelRows + r;
+                sc0 = __ldg(sp);
+                sc1 = kb + 1 < KB ? __ldg(sp + kPanelRows) : 0;
+            };
+            scales_of();
             for (int g = 0; g < nu; ++g) {
-                const int st = 2 * g + 1, ss = g % kPfSS; // the group's last step
+                const int st = 2 * g + 1; // the group's last step
+                const float s = bf16_bits_to_float(sc0);
+                sc0 = sc1;
+                if (kb + 2 < KB)
+                    sc1 = __ldg(sp + 2 * kPanelRows);
+                sp += kPanelRows;
+                ++kb;
+                bool end = kb == KB || g == nu - 1;
                 // A warp whose wait gave up goes on without waiting, so that every
                 // warp of the group comes to the barriers of every tile.
-                ok = ok && mbar_wait_warp(&done[st % XS], (st / XS) & 1) &&
-                     mbar_wait_warp(&sfull[ss], (g / kPfSS) & 1);
+                ok = ok && mbar_wait_warp(&done[st % XS], (st / XS) & 1);
                 tc_fence_after();
-                const float s = bf16_bits_to_float(reinterpret_cast<const uint16_t *>(sS + ss * 256)[r]);
                 unsigned long long s2;
                 asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
                 const uint32_t ta = tq + (g & 1) * kPfTok;
@@ -758,21 +768,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                     tmem_ld_32x32b_x16(ta + 16 * c, v[0]);
                     tmem_ld_32x32b_x16(ta + 16 * c + 16, v[1]);
                     tmem_wait_ld();
+                    if (c + 2 == C::kChunks) { // every column is read: released before the last are used
+                        tc_fence_before();
+                        __syncwarp();
+                        pf_arrive(rt.ebar + (g & 1) * 8, lane == 0 && !end);
+                    }
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int j = 0; j < 16; j += 2)
                             pf_ffma2(tot[8 * (c + e) + j / 2], s2, v[e][j], v[e][j + 1]);
                 }
-                __syncwarp();
-                pf_arrive_own(&sempty[ss], lane == 0);
-                const bool end = ++kb == KB;
-                if (!end && g < nu - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    pf_arrive(rt.ebar + (g & 1) * 8, lane == 0);
+                if (!end)
                     continue;
-                }
                 // the tile's (or the run's) last group: the totals take its
                 // accumulator's place, so that writing them out needs few registers
 #pragma unroll
@@ -795,6 +803,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                     tot[j] = 0ull;
                 kb = 0;
                 ++tile;
+                if (g < nu - 1)
+                    scales_of();
             }
         } else {
             const int tile1 = nu > 0 ? (u1 - 1) / KB : tile0 - 1;
