@@ -256,10 +256,11 @@ typedef struct {
  *   ws        a workspace of ws_bytes for this call, as wq_linear_ex (zeroed by
  *             the caller before its first use; calls that share one must not
  *             overlap), or NULL: the registered one
- * Up to 128 tokens the kernel is the dispatcher's (a tuned entry, as in
- * wq_linear), or the prompt GEMM where a rule on the sizes finds it faster; above
- * 128 the prompt GEMM takes all tokens in one launch (INT4 groups stored as 128;
- * other groups run 128 tokens at a time).  Neither fails for lack of workspace.
+ * Up to 128 tokens the kernel is the dispatcher's, as in wq_linear, or the
+ * prompt GEMM where a rule on the sizes finds it faster and wq_set_choice has not
+ * named another; above 128 the prompt GEMM takes all tokens in one launch (INT4
+ * groups stored as 128; other groups run 128 tokens at a time).  The prompt GEMM
+ * uses as much of the workspace as it finds and needs none.
  * WQ_ERR_EPILOGUE for an unknown act or a row stride below N. */
 int wq_linear_epilogue(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
                        const void *zeros, int group, int N, const wq_epilogue *epilogue,

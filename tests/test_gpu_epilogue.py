@@ -333,3 +333,126 @@ def test_feed_forward_run():
     check(g, x, wg, None, "silu", None, None, torch.bfloat16)
     check(h, x, wu, None, "none", g, None, torch.bfloat16)
     check(out, h, wd, None, "none", None, before, torch.bfloat16)
+
+
+@pytest.mark.parametrize("bits,group,M", [(8, 0, 4000), (4, 128, 3000), (8, 0, 6000)])
+def test_many_tiles_a_pair(bits, group, M):
+    """Every pair of CTAs writes several tiles out, each behind the next one's products."""
+    K, N = 256, 2064
+    pw, w = make_weight(bits, group, K, N)
+    x, bias, mul, res = operands(M, K, N, torch.bfloat16)
+    for ws in (ws_for(M, K, N), None):
+        y = wq.wq_linear_epilogue(x, pw, bias=bias, act=wq.WQ_ACT_RELU, mul=mul, residual=res, ws=ws)
+        check(y, x, w, bias, "relu", mul, res, torch.bfloat16)
+    assert wq.wq_device_error() == 0
+
+
+def test_prompts_and_decode_steps_in_graphs_that_share_a_workspace():
+    K, N = 2048, 528
+    pw8, w8 = make_weight(8, 0, K, N)
+    pw4, w4 = make_weight(4, 128, K, N)
+    ws = ws_for(300, K, N)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    runs = []
+    for i, (pw, w, M) in enumerate([(pw8, w8, 300), (pw4, w4, 5), (pw4, w4, 300), (pw8, w8, 1), (pw4, w4, 64)]):
+        x, bias, mul, res = operands(M, K, N, torch.bfloat16, i)
+        wq.wq_linear_epilogue(x, pw, residual=res, ws=ws, stream=s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            y = wq.wq_linear_epilogue(x, pw, bias=bias, mul=mul, residual=res, ws=ws)
+        runs.append((g, y, x, w, bias, mul, res))
+    for order in ((0, 1, 2, 3, 4), (4, 2, 0, 1, 3), (2, 2, 0, 0, 4)):
+        for i in order:
+            runs[i][2].copy_(torch.roll(runs[i][2], 1, 0))
+            runs[i][0].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            _, y, x, w, bias, mul, res = runs[i]
+            check(y, x, w, bias, "none", mul, res, torch.bfloat16)
+    assert int(ws[:262912].max()) == 0
+    assert wq.wq_device_error() == 0
+
+
+@pytest.mark.parametrize("M", [4, 200])
+def test_two_calls_at_once(M):
+    """On two streams, each with its own workspace."""
+    K, N = 2048, 1040
+    pw, w = make_weight(4, 128, K, N)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets = [(operands(M, K, N, torch.bfloat16, i), ws_for(M, K, N)) for i in range(2)]
+    torch.cuda.synchronize()
+    out = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            (x, bias, mul, res), ws = sets[i]
+            out[i].append(wq.wq_linear_epilogue(x, pw, bias=bias, mul=mul, residual=res, ws=ws, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        (x, bias, mul, res), _ = sets[i]
+        for y in out[i]:
+            check(y, x, w, bias, "none", mul, res, torch.bfloat16)
+
+
+def test_a_tuned_table_and_a_chosen_kernel():
+    """wq_tune's entry (the plain layer's fastest kernel) and wq_set_choice's are
+    both good for calls with an epilogue."""
+    M, K, N = 32, 1024, 528
+    pw, w = make_weight(8, 0, K, N)
+    x, bias, mul, res = operands(M, K, N, torch.bfloat16)
+    ws = ws_for(M, K, N)
+    wq.wq_set_workspace(ws)
+    try:
+        wq.wq_tune(x, pw, torch.empty((M, N), dtype=torch.bfloat16, device=dev()), warmup=1, iters=2)
+        y = wq.wq_linear_epilogue(x, pw, bias=bias, residual=res)
+        check(y, x, w, bias, "none", None, res, torch.bfloat16)
+        wq.wq_set_choice(M, K, N, 8, 0, wq.WQ_VARIANT_GEMV_RB, 4)
+        y = wq.wq_linear_epilogue(x, pw, bias=bias, residual=res)
+        check(y, x, w, bias, "none", None, res, torch.bfloat16)
+    finally:
+        wq.wq_clear_tuning()
+        wq.wq_set_workspace(None)
+
+
+@pytest.mark.parametrize("M", [1, 6, 150])
+def test_decode_step_to_log_probabilities(M):
+    """The layers of a step and the vocabulary head's log probabilities behind
+    them, captured together and replayed with another input; the same bits as the
+    calls one by one."""
+    D, H, V, k = 512, 1024, 3088, 5
+    gate, up = make_weight(4, 128, D, H, 1)[0], make_weight(4, 128, D, H, 2)[0]
+    down, head = make_weight(8, 0, H, D, 3)[0], make_weight(8, 0, D, V, 4)[0]
+    ws = ws_for(max(M, 64), H, V)
+    scratch = torch.empty(wq.wq_linear_logprobs_workspace_bytes(M, V), dtype=torch.uint8, device=dev())
+    x = operands(M, D, H, torch.bfloat16)[0]
+    t = torch.arange(M, dtype=torch.int32, device=dev()) * 7 % V
+
+    def step():
+        g = wq.wq_linear_epilogue(x, gate, act=wq.WQ_ACT_SILU, ws=ws)
+        h = wq.wq_linear_epilogue(x, up, mul=g, ws=ws)
+        y = wq.wq_linear_epilogue(h, down, residual=x, ws=ws)
+        return (y, *wq.wq_linear_logprobs(y, head, t, k, scratch, ws=ws))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        captured = step()
+    for seed in (11, 12):
+        x.copy_(operands(M, D, H, torch.bfloat16, seed)[0])
+        g.replay()
+        torch.cuda.synchronize()
+        once = step()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, once):
+            assert torch.equal(a, b)
+        y, lp, ent, top, idx = once
+        assert bool((top[:, 1:] <= top[:, :-1]).all()) and bool((top <= 0).all()) and bool((lp <= top[:, 0]).all())
+        assert bool((ent >= 0).all()) and bool((ent <= math.log(V) + 2 ** -17 * (2 + math.log(V))).all())
+        # the alternatives' own log probabilities, asked for as tokens
+        again = wq.wq_linear_logprobs(y, head, idx[:, 1].contiguous(), 0, scratch, ws=ws)[0]
+        assert torch.equal(again, top[:, 1])
+    assert wq.wq_device_error() == 0

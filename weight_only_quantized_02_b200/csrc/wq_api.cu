@@ -322,7 +322,7 @@ int linear_prompt(const uint16_t *x, int M, int K, const void *Wq, const void *s
                   const EpiArgs &epi);
 
 // Whether a call with an epilogue and at most 128 tokens goes to the prompt
-// GEMM, without an entry of the dispatcher's table for it.  Measured on B200, us,
+// GEMM, unless the caller chose a kernel for these sizes.  Measured on B200, us,
 // the layer's other kernels | the prompt GEMM:
 //   INT8, 5120 x 17408: M = 9 28 | 31, 16 41 | 31, 64 92 | 32, 128 51 | 35;
 //   17408 x 5120: M = 9 43 | 40, 64 178 | 48; 1024 x 1024: M = 9 16 | 12, 64 62 | 13;
@@ -363,13 +363,17 @@ bool f16_prompt_faster(int bits, int M, int K, int N, int sm_count)
     return 5 + rounds * blocks * (bits == 8 ? 0.61 : 0.8) < gemv;
 }
 
-bool tuned(int M, int K, int N, int bits, int group)
+// Whether the caller chose the kernel for these sizes (wq_set_choice).  An entry
+// with a time is wq_tune's, the fastest of the plain layer's kernels: which of them
+// is taken where the rule above says none of them is, is not its matter.
+bool chosen(int M, int K, int N, int bits, int group)
 {
     DeviceInfo d;
     if (current_device_info(&d) != WQ_OK)
         return false;
     std::lock_guard<std::mutex> lk(g_mu);
-    return g_table.count(Key{device_key(d), M, K, N, bits, group}) != 0;
+    const auto it = g_table.find(Key{device_key(d), M, K, N, bits, group});
+    return it != g_table.end() && it->second.us == 0.f;
 }
 
 // The epilogue of the token rows from m0 on.
@@ -398,7 +402,7 @@ int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *sca
         return WQ_ERR_GROUP;
     const int chunk = chunk_tokens(bits, lgroup_of(bits, K, group));
     if (epi && chunk == kChunkTokens && variant == WQ_VARIANT_AUTO &&
-        (M > kChunkTokens || (prompt_faster(bits, M, K, N) && !tuned(M, K, N, bits, group))))
+        (M > kChunkTokens || (prompt_faster(bits, M, K, N) && !chosen(M, K, N, bits, group))))
         return linear_prompt(x, M, K, Wq, scales, zeros, bits, group, N, y, ws, ws_bytes_given, stream, *epi);
     if (M <= chunk)
         return linear_chunk(x, M, K, Wq, scales, zeros, group, N, y, variant, split, ws, ws_bytes_given, stream, epi);

@@ -35,7 +35,11 @@
 // with them.  A logit is ranked by a 64-bit key (value, then the complement of
 // its index), so all keys differ and the answer is unique.
 // (Collecting during the loop, against a bound raised as it went, took 307 us
-// for 2048 rows of 152064 logits and k = 5, against 127 without alternatives.)
+// for 2048 rows of 152064 logits and k = 5.)
+//
+// Measured on B200: 2048 rows of 152064 bf16 logits 114 us without alternatives
+// (5.5 TB/s), 135 with 5 and 150 with 64; one such row with 20 alternatives 8.6; 77
+// rows of 50001 fp32 logits with 64 15.3.
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
