@@ -46,12 +46,15 @@
 //
 // Measured on B200 (layer with a residual or the other half of a gate, the weights
 // in L2): INT4 17408 x 5120, 2048 tokens 357 us (1020 TFLOP/s); 5120 x 17408, 364
-// tokens 82; INT8 17408 x 5120, 2048 tokens 314 (1170 TFLOP/s; the tensor pipe busy
-// in 98 % of the cycles, at a clock that the power limit holds at 1.0 to 1.4 GHz);
-// 5120 x 17408, 333 tokens 58.  INT4 is held by the work beside the products: a unit
-// takes some 1350 cycles against 768 of products at 192 tokens, the dequantization
-// about 1200 of its warps' time and the retirement 900, both by instruction
-// latency at one or two warps a scheduler.
+// tokens 82; INT8 17408 x 5120, 2048 tokens 314 (1170 TFLOP/s); 5120 x 17408, 333
+// tokens 58.  In one launch of 2048 tokens the tensor pipe is busy in 70 % of the
+// cycles for INT8, at 1.57 GHz (back to back, the power limit holds the clock
+// between 1.0 and 1.4 and the pipe is nearly always busy), and in 51 % for INT4, at
+// 1.66 GHz.  INT4 is held by the work beside the products: a unit takes some 1350
+// cycles against 768 of products at 192 tokens, the dequantization about 1200 of its
+// warps' time and the retirement 900, both by instruction latency at one or two
+// warps a scheduler; neither alone (a third of the retirement 320 us, no conversion
+// of the codes 327).
 //
 // Every wait is bounded (2 s); a timeout is recorded and every role winds down.
 #include <atomic>
