@@ -456,3 +456,24 @@ def test_decode_step_to_log_probabilities(M):
         again = wq.wq_linear_logprobs(y, head, idx[:, 1].contiguous(), 0, scratch, ws=ws)[0]
         assert torch.equal(again, top[:, 1])
     assert wq.wq_device_error() == 0
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bits,group,M", [(8, 0, 2), (4, 128, 40), (8, 0, 150)])
+def test_activations_over_their_range(bits, group, M, dtype, act):
+    """No product: the bias alone goes through the activation, from -12.5 (where
+    erfc is 7e-36) to 12.5, and the largest finite values on both sides, where the
+    answer is 0 or the value itself."""
+    K, N = 128, 4096
+    pw, w = make_weight(bits, group, K, N)
+    x = torch.zeros((M, K), dtype=dtype, device=dev())
+    bias = torch.linspace(-12.5, 12.5, N, device=dev()).to(dtype)
+    bias[:2] = torch.tensor([-torch.finfo(dtype).max, torch.finfo(dtype).max], dtype=dtype)
+    if dtype == torch.bfloat16:
+        y = wq.wq_linear_epilogue(x, pw, bias=bias, act=ACTS[act], ws=ws_for(M, K, N))
+    else:
+        y = wq.wq_linear_epilogue_f16(x, pw, bias=bias, act=ACTS[act])
+    ends = [0.0 if act != "none" else -torch.finfo(dtype).max, torch.finfo(dtype).max]
+    assert torch.equal(y[:, :2].double(), torch.tensor([ends] * M, dtype=torch.float64, device=dev()))
+    check(y[:, 2:], x, w[2:], bias[2:], act, None, None, dtype)

@@ -63,6 +63,29 @@ __device__ __forceinline__ uint16_t float_to_act16(float v)
         return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// erfc(a) for a >= 0: t exp(-a^2 + P(t)), t = 1 / (1 + a / 2) (the substitution of
+// Press et al., Numerical Recipes, 6.2), P a Chebyshev fit of ln(erfc(a) exp(a^2) / t)
+// over 0 < t <= 1 in powers of t.  Relative error, by evaluation in fp32 against
+// binary64 for a up to 9: 4.1e-7 near 0, then that of the exponential's argument,
+// together at most (2 + 1.4 a^2) 2^-22 with the fast exponential's.  Straight code,
+// for several values side by side (prompt GEMM, INT8 5120 x 17408, 333 tokens: 59 us
+// against 66 with erfcf).
+__device__ __forceinline__ float epi_erfc(float a)
+{
+    const float t = __fdividef(1.f, fmaf(0.5f, a, 1.f));
+    float p = 0.170868918f;
+    p = fmaf(p, t, -0.822135866f);
+    p = fmaf(p, t, 1.48848701f);
+    p = fmaf(p, t, -1.13517654f);
+    p = fmaf(p, t, 0.278852999f);
+    p = fmaf(p, t, -0.186283216f);
+    p = fmaf(p, t, 0.0967833176f);
+    p = fmaf(p, t, 0.374092042f);
+    p = fmaf(p, t, 1.00002372f);
+    p = fmaf(p, t, -1.26551223f);
+    return t * __expf(fmaf(-a, a, p));
+}
+
 // The activation of CNT values.  The erf form is written with erfc, which keeps
 // its relative accuracy where 1 + erf cancels; the tanh form is v * logistic(2 u),
 // which does not cancel either.  The logistic function uses the fast exponential
@@ -79,8 +102,10 @@ __device__ __forceinline__ void epi_activations(float (&v)[CNT], int act)
             v[j] = v[j] < 0.f ? 0.f : v[j];
     } else if (act == WQ_ACT_GELU) {
 #pragma unroll
-        for (int j = 0; j < CNT; ++j)
-            v[j] = 0.5f * v[j] * erfcf(-0.70710678f * v[j]);
+        for (int j = 0; j < CNT; ++j) {
+            const float e = epi_erfc(0.70710678f * fabsf(v[j]));
+            v[j] = 0.5f * v[j] * (v[j] > 0.f ? 2.f - e : e);
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < CNT; ++j) {
