@@ -114,6 +114,44 @@ def test_masked_rows(dtype, M, N):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,k", [(9, 50001, 20), (1, 152064, 64), (3, 9000, 64)])
+@pytest.mark.parametrize("mask", [-math.inf, "lowest"])
+def test_fewer_logits_left_than_alternatives(dtype, M, N, k, mask):
+    """Row m keeps m + 1 logits; the alternatives behind them are the first masked ones."""
+    x, t = rows(M, N, dtype, 5)
+    keep = torch.zeros((M, N), dtype=torch.bool, device=dev())
+    for m in range(M):
+        keep[m, (torch.arange(m + 1) * 7919 + 13 * m + 40) % N] = True
+    x[~keep] = torch.finfo(dtype).min if mask == "lowest" else mask
+    lp, H, top, idx = wq.wq_logprobs(x, t, k)
+    rl, rH, rt, ri = reference(x, t, k)
+    assert torch.equal(idx, ri)
+    close(H, rH, 2 + rH.abs())
+    same = (lp.double() == rl) | ((lp.double() - rl).abs() <= 2.0 ** -17 + 2.0 ** -22 * rl.abs())
+    assert bool(same.all())
+    same = (top.double() == rt) | ((top.double() - rt).abs() <= 2.0 ** -17 + 2.0 ** -22 * rt.abs()) | \
+        (top.isinf() & (rt < -3.4e38))
+    assert bool(same.all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,k", [(4, 50001, 64), (1, 152064, 20), (700, 12000, 5), (200, 40000, 33)])
+@pytest.mark.parametrize("above", [3, 40, 1500, 6000])
+def test_many_equal_logits_below_some(dtype, M, N, k, above):
+    """Most logits equal, `above` of them (anywhere in the row) of a few larger
+    values, one row of them all of one value: the k-th largest is the common value,
+    among the larger ones, or one of many equal larger ones."""
+    g = torch.Generator(device=dev()).manual_seed(above)
+    x = torch.full((M, N), -2.0, device=dev())
+    at = torch.randint(0, N, (M, above), generator=g, device=dev())
+    x.scatter_(1, at, torch.randint(0, 4000, (M, above), generator=g, device=dev()).float() / 500)
+    x[0].clamp_(max=-1.0)
+    x = x.to(dtype)
+    t = at[:, 0].int().contiguous()
+    check(x, t, k, wq.wq_logprobs(x, t, k))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N", [100, 40000])
 def test_rows_without_a_distribution(dtype, N):
     x, t = rows(5, N, dtype, 2)

@@ -580,6 +580,48 @@ __device__ __noinline__ void first_equal(const Slice<T, THREADS> &sl, Shared &sh
     }
 }
 
+// For a slice with many logits equal to `bound` (a mask that leaves few others),
+// which at least k logits reach: lists those above it, from the runs that hold one,
+// and the first of the equal ones behind them.  Returns the list's length, at
+// least k, or 0 if there are too many above it, too.
+template <class T, int THREADS, class Shared>
+__device__ __noinline__ int list_above(const Slice<T, THREADS> &sl, Shared &sh, uint32_t bound, int k,
+                                       const float *runs, int per_run, int n_runs)
+{
+    __syncthreads(); // every thread has read sh.chosen_count
+    if (threadIdx.x == 0)
+        sh.chosen_count = 0;
+    __syncthreads();
+    const float of = value32(bound);
+    for (int i = 0; i < n_runs; ++i)
+        if (runs[i * THREADS] > of) {
+            const int at = atomicAdd(&sh.chosen_count, 1);
+            if (at < kChosenMax)
+                sh.chosen[at] = (uint32_t)i << 16 | threadIdx.x;
+        }
+    __syncthreads();
+    if (sh.chosen_count > kChosenMax)
+        return 0;
+    each_above(sl, sh, per_run, bound, false, [&](uint32_t o, int idx) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kListMax)
+            sh.list[at] = ((key_t64)o << 32) | (uint32_t)~idx;
+    });
+    __syncthreads();
+    const int n = sh.count;
+    if (n > kListMax) {
+        __syncthreads();
+        if (threadIdx.x == 0)
+            sh.count = 0; // the caller's
+        return 0;
+    }
+    if (n >= k)
+        return n;
+    first_equal(sl, sh, bound, n, k - n);
+    __syncthreads();
+    return k;
+}
+
 // The slice's k best, in order, into sh.best.  mine: order32 that the largest
 // logit this thread read reaches, 0 if it read none; top: no logit is above it;
 // runs: the largest of each run of per_run vectors this thread read, THREADS
@@ -611,8 +653,19 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
         }
     }
     __syncthreads();
+    const int n_runs = (all + per_run - 1) / per_run;
+    bool few_above = top != kOrderNan; // perhaps; the same for every thread, as nan is not
     int per = per_run;
-    if (sh.chosen_count > kChosenMax) { // too many runs: the chosen threads' whole columns
+    if (sh.chosen_count > kChosenMax) {
+        if (few_above) {
+            const int n = list_above(sl, sh, bound, k, runs, per_run, n_runs);
+            if (n) {
+                sort_list(sh, n, k);
+                return;
+            }
+            few_above = false;
+        }
+        // too many runs: the chosen threads' whole columns
         per = all;
         __syncthreads();
         if (threadIdx.x == 0)
@@ -623,6 +676,8 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
         __syncthreads();
     }
     each_above(sl, sh, per, bound, true, [&](uint32_t o, int idx) {
+        if (*(volatile int *)&sh.count > kListMax)
+            return; // too many already: a masked row's thousands would queue for the counter
         const int at = atomicAdd(&sh.count, 1);
         if (at < kListMax)
             sh.list[at] = ((key_t64)o << 32) | (uint32_t)~idx;
@@ -630,8 +685,19 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
     __syncthreads();
     int n = sh.count;
     if (n > kListMax) {
-        // the k-th largest value: the largest that at least k elements reach
-        uint32_t lo = bound, hi = top;
+        if (few_above) {
+            __syncthreads(); // every thread has read sh.count
+            if (threadIdx.x == 0)
+                sh.count = 0;
+            n = list_above(sl, sh, bound, k, runs, per_run, n_runs);
+            if (n) {
+                sort_list(sh, n, k);
+                return;
+            }
+        }
+        // the k-th largest value: the largest that at least k elements reach (more
+        // than k are above the bound, and in the runs chosen now, if few_above)
+        uint32_t lo = few_above ? bound + 1 : bound, hi = top;
         int slot = 0;
         while (lo < hi) {
             const uint32_t mid = hi - (hi - lo) / 2;
