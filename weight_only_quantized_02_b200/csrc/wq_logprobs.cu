@@ -28,18 +28,20 @@
 // step) is reached by at least k logits, and only those threads' logits can be
 // among the k largest; of those, the runs of vectors whose largest (kept in shared
 // memory, at most 32 a thread) reaches it.  They are read again, by all threads
-// together, and what reaches the value is kept and ranked.  Where more
-// reaches it than the list holds (rows of few distinct values, masks) the k-th
-// largest value is found by counting over those vectors, everything above it
-// kept, and of the logits equal to it the first in the row, by a scan that ends
-// with them.  A logit is ranked by a 64-bit key (value, then the complement of
+// together, and what reaches the value is kept and ranked.  Where much of the row
+// shares the value (a mask that leaves fewer logits than alternatives) only what is
+// above it is read again, and of the logits equal to it the first in the row, by a
+// scan that ends with them.  Where more reaches it than the list holds all the same
+// (rows of few distinct values) the k-th largest value is found by counting over
+// those vectors.  A logit is ranked by a 64-bit key (value, then the complement of
 // its index), so all keys differ and the answer is unique.
 // (Collecting during the loop, against a bound raised as it went, took 307 us
 // for 2048 rows of 152064 logits and k = 5.)
 //
 // Measured on B200: 2048 rows of 152064 bf16 logits 114 us without alternatives
-// (5.5 TB/s), 135 with 5 and 150 with 64; one such row with 20 alternatives 8.6; 77
-// rows of 50001 fp32 logits with 64 15.3.
+// (5.5 TB/s), 118 with 5 and 135 with 64 (168 with 5 where a mask leaves a few logits
+// a row); one such row with 20 alternatives 8.6; 77 rows of 50001 fp32 logits with 64
+// 15.5.
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
@@ -332,10 +334,12 @@ __device__ __forceinline__ key_t64 cluster_ld_u64(uint32_t a)
 
 // A value that at least k of the threads' keys reach, and at most lp_accept(k)
 // of them unless too many are equal to the k-th largest; 0 if fewer than k
-// threads have a key.  top: no key is above it.  Called by the whole CTA.
-__device__ __forceinline__ uint32_t bound_of_threads(uint32_t mine, uint32_t top, int k)
+// threads have a key.  top: no key is above it.  reach: the threads that reach it.
+// Called by the whole CTA.
+__device__ __forceinline__ uint32_t bound_of_threads(uint32_t mine, uint32_t top, int k, int &reach)
 {
-    if (__syncthreads_count(mine != 0) < k)
+    reach = __syncthreads_count(mine != 0);
+    if (reach < k)
         return 0;
     // from the top down in growing steps (the maxima of many logits lie close
     // together), then by halves
@@ -346,6 +350,8 @@ __device__ __forceinline__ uint32_t bound_of_threads(uint32_t mine, uint32_t top
         if (lo == 0 && step < hi - mid)
             mid = hi - step;
         const int c = __syncthreads_count(mine >= mid);
+        if (c >= k)
+            reach = c;
         if (c >= k && c <= lp_accept(k))
             return mid;
         if (c < k) {
@@ -632,7 +638,8 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
 {
     if (threadIdx.x == 0)
         sh.chosen_count = sh.count = 0;
-    const uint32_t bound = bound_of_threads(mine, min(top, kOrderInf), k); // has a barrier
+    int reach;
+    const uint32_t bound = bound_of_threads(mine, min(top, kOrderInf), k, reach); // has a barrier
     const int all = (sl.nv + THREADS - 1) / THREADS; // vectors of a thread, at most
     const bool chosen = mine != 0 && mine >= bound;
     if (chosen) {
@@ -653,18 +660,20 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
         }
     }
     __syncthreads();
-    const int n_runs = (all + per_run - 1) / per_run;
-    bool few_above = top != kOrderNan; // perhaps; the same for every thread, as nan is not
     int per = per_run;
-    if (sh.chosen_count > kChosenMax) {
-        if (few_above) {
-            const int n = list_above(sl, sh, bound, k, runs, per_run, n_runs);
-            if (n) {
-                sort_list(sh, n, k);
-                return;
-            }
-            few_above = false;
+    bool columns = sh.chosen_count > kChosenMax;
+    // Many threads reach the bound and none could be told from another: a value that
+    // much of the row shares.  (16-bit logits at large have ties, too, but not of three
+    // threads in four.)
+    if (top != kOrderNan && (columns || (bound != 0 && reach > lp_accept(k) && reach > THREADS * 3 / 4))) {
+        const int n = list_above(sl, sh, bound, k, runs, per_run, (all + per_run - 1) / per_run);
+        if (n) {
+            sort_list(sh, n, k);
+            return;
         }
+        columns = true;
+    }
+    if (columns) {
         // too many runs: the chosen threads' whole columns
         per = all;
         __syncthreads();
@@ -685,19 +694,8 @@ __device__ __forceinline__ void select_best(const Slice<T, THREADS> &sl, Shared 
     __syncthreads();
     int n = sh.count;
     if (n > kListMax) {
-        if (few_above) {
-            __syncthreads(); // every thread has read sh.count
-            if (threadIdx.x == 0)
-                sh.count = 0;
-            n = list_above(sl, sh, bound, k, runs, per_run, n_runs);
-            if (n) {
-                sort_list(sh, n, k);
-                return;
-            }
-        }
-        // the k-th largest value: the largest that at least k elements reach (more
-        // than k are above the bound, and in the runs chosen now, if few_above)
-        uint32_t lo = few_above ? bound + 1 : bound, hi = top;
+        // the k-th largest value: the largest that at least k elements reach
+        uint32_t lo = bound, hi = top;
         int slot = 0;
         while (lo < hi) {
             const uint32_t mid = hi - (hi - lo) / 2;
