@@ -21,6 +21,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,6 +30,18 @@
 #include "wq_internal.h"
 
 namespace wq {
+
+// A kernel's parameters, with an epilogue or without.  The instances without one
+// have nothing of it, parameters and stores included, so that they are compiled as
+// if there were none: with it among the parameters, and stores shared by both forms,
+// the integer GEMV of 5120 x 17408 took 21.6 us at four tokens instead of 19.9, the
+// role-split GEMM of 17408 x 5120 33.9 at 64 instead of 32.3.
+template <class Params>
+struct WithEpilogue : Params {
+    EpiArgs epi;
+};
+template <class Params, bool EPI>
+using EpiParams = std::conditional_t<EPI, WithEpilogue<Params>, Params>;
 
 // The two tensor operands of one output, as loaded: converted only where they
 // are used.  A thread with several outputs asks once whether an operand is there
@@ -223,26 +236,6 @@ __device__ __forceinline__ void epi_store64(const EpiArgs &e, uint16_t *y, int N
         epi_store<true>(e, y, N, m, n, (float)v, bias, o);
     else
         y[(size_t)m * N + n] = __bfloat16_as_ushort(__double2bfloat16(v));
-}
-
-// Outputs (m0 + j, n), j = 0 .. CNT-1 of which the first jn exist, of one
-// thread that holds CNT tokens of output channel n: operands in flight
-// together, B tokens at a time.
-template <bool EPI, int CNT, int B = (CNT < 16 ? CNT : 16)>
-__device__ __forceinline__ void epi_store_tokens(const EpiArgs &e, uint16_t *y, int N, int m0, int jn, int n,
-                                                 const float (&v)[CNT])
-{
-    static_assert(CNT % B == 0, "whole batches");
-    const float bias = epi_bias<EPI>(e, n);
-#pragma unroll
-    for (int j0 = 0; j0 < CNT; j0 += B) {
-        EpiOps o[B];
-        epi_load_tokens<EPI>(e, o, m0 + j0, jn - j0, n);
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-            if (j0 + j < jn)
-                epi_store<EPI>(e, y, N, m0 + j0 + j, n, v[j0 + j], bias, o[j]);
-    }
 }
 
 } // namespace wq

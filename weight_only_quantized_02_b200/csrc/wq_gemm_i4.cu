@@ -59,7 +59,6 @@ struct I4Params {
     const uint16_t *scales; // [P][KB][128] bf16
     const uint8_t *zeros;   // [P][KB][64]: row i at nibble i
     uint16_t *y;
-    EpiArgs epi; // the EPI instances' epilogue
     uint8_t *xd;            // [KB][NR][128] digit blocks
     float *part;            // [G][2 slots][NR/3 tokens][128 rows] fp32
     uint32_t *cnt;          // [panels][4] tickets
@@ -127,19 +126,17 @@ __device__ __forceinline__ void umma_ts_i8(uint32_t d_tmem, uint32_t a_tmem, uin
 
 // The epilogue operands of output channel n and every token, loaded together;
 // returns the channel's bias.
-template <bool EPI, int MM>
-__device__ __forceinline__ float i4_epi_ops(const I4Params &p, int n, int M, EpiOps (&ops)[MM])
+template <int MM>
+__device__ __forceinline__ float i4_epi_ops(const EpiArgs &e, int N, int n, int M, EpiOps (&ops)[MM])
 {
-    epi_load_tokens<EPI>(p.epi, ops, 0, n < p.N ? M : 0, n);
-    if (n >= p.N)
-        return 0.f;
-    return epi_bias<EPI>(p.epi, n);
+    epi_load_tokens<true>(e, ops, 0, n < N ? M : 0, n);
+    return n < N ? epi_bias<true>(e, n) : 0.f;
 }
 
 template <int NR, bool EPI>
 // 14 warps: at most 4 per SM sub-partition, whose register file holds 16K
 // registers, so at most 128 per thread.
-__global__ void __maxnreg__(128) gemm_i4_kernel(const I4Params p)
+__global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p)
 {
     using C = I4Cfg<NR>;
     constexpr int SP = C::kPStages, SD = C::kDStages, SA = C::kAStages, TB = C::kTB;
@@ -408,14 +405,20 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const I4Params p)
                     const int lo = max(u0, pnl * KB), hi = min(u1, (pnl + 1) * KB);
                     if (lo == pnl * KB && hi == (pnl + 1) * KB) {
                         EpiOps ops[MM];
-                        const float bias = i4_epi_ops<EPI, MM>(p, pnl * kPanelRows + row, M, ops);
+                        float bias = 0.f;
+                        if constexpr (EPI)
+                            bias = i4_epi_ops(p.epi, p.N, pnl * kPanelRows + row, M, ops);
 #pragma unroll
                         for (int m = 0; m < MM; ++m)
                             if (m < M) // the same across the warp
-                                imma_emit_rows<4, EPI>(p.x, p.wq, p.scales, p.zeros, p.epi, p.y, p.K, KB, p.N,
-                                                       pnl * kPanelRows + 32 * quad, m,
-                                                       (double)acc[m] * pow2_of(-s_e[m]), wmax * s_rb[m], bias, ops[m],
-                                                       lane);
+                                imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.K, KB, p.N,
+                                                  pnl * kPanelRows + 32 * quad, m, (double)acc[m] * pow2_of(-s_e[m]),
+                                                  wmax * s_rb[m], lane, [&](int n, double y) {
+                                    if constexpr (EPI)
+                                        epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[m]);
+                                    else
+                                        p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
+                                });
                         break;
                     }
                     const int slot = (pnl == sk.first[c]) ? 0 : 1;
@@ -449,13 +452,20 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const I4Params p)
                             tot[m] += v[m];
                     }
                     EpiOps ops[MM];
-                    const float bias = i4_epi_ops<EPI, MM>(p, pnl * kPanelRows + row, M, ops);
+                    float bias = 0.f;
+                    if constexpr (EPI)
+                        bias = i4_epi_ops(p.epi, p.N, pnl * kPanelRows + row, M, ops);
 #pragma unroll
                     for (int m = 0; m < MM; ++m)
                         if (m < M) // the same across the warp
-                            imma_emit_rows<4, EPI>(p.x, p.wq, p.scales, p.zeros, p.epi, p.y, p.K, KB, p.N,
-                                                   pnl * kPanelRows + 32 * quad, m, (double)tot[m] * pow2_of(-s_e[m]),
-                                                   wmax * s_rb[m], bias, ops[m], lane);
+                            imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.K, KB, p.N,
+                                              pnl * kPanelRows + 32 * quad, m, (double)tot[m] * pow2_of(-s_e[m]),
+                                              wmax * s_rb[m], lane, [&](int n, double y) {
+                                if constexpr (EPI)
+                                    epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[m]);
+                                else
+                                    p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
+                            });
                     if (lane == 0)
                         atomicExch(&p.cnt[pnl * 4 + quad], 0u);
                 } while (false);
@@ -515,7 +525,7 @@ static cudaError_t launch_i4_e(const LinearArgs &a, void *ws, int sm_count, cuda
             return e;
     }
     const Shape sh{4, a.K, a.N, 128};
-    I4Params p;
+    EpiParams<I4Params, EPI> p;
     p.x = a.x;
     p.M = a.M;
     p.K = a.K;
@@ -526,7 +536,8 @@ static cudaError_t launch_i4_e(const LinearArgs &a, void *ws, int sm_count, cuda
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
-    p.epi = a.epi ? *a.epi : EpiArgs{};
+    if constexpr (EPI)
+        p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.grid = p.cnt + ws_grid_counter();
     p.res = reinterpret_cast<unsigned long long *>(p.cnt + ws_res_counter());

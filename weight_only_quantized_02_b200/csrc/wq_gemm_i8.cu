@@ -67,7 +67,6 @@ struct I8Params {
     const uint8_t *wq;
     const uint16_t *scales;
     uint16_t *y;
-    EpiArgs epi; // the EPI instances' epilogue
     uint8_t *xd;    // [KB][NR][128] digit blocks
     int32_t *part;  // [G][2 slots][NR][128 rows] int32
     uint32_t *cnt;  // [panels][4] tickets
@@ -107,17 +106,15 @@ constexpr size_t i8_smem_bytes()
 
 // The epilogue operands of output channel n and tokens m0 .. m0 + CNT - 1,
 // loaded together; returns the channel's bias.
-template <bool EPI, int CNT>
-__device__ __forceinline__ float i8_epi_ops(const I8Params &p, int n, int m0, int M, EpiOps (&ops)[CNT])
+template <int CNT>
+__device__ __forceinline__ float i8_epi_ops(const EpiArgs &e, int N, int n, int m0, int M, EpiOps (&ops)[CNT])
 {
-    epi_load_tokens<EPI>(p.epi, ops, m0, n < p.N ? M - m0 : 0, n);
-    if (n >= p.N)
-        return 0.f;
-    return epi_bias<EPI>(p.epi, n);
+    epi_load_tokens<true>(e, ops, m0, n < N ? M - m0 : 0, n);
+    return n < N ? epi_bias<true>(e, n) : 0.f;
 }
 
 template <int NR, bool EPI>
-__global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(const I8Params p)
+__global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(const EpiParams<I8Params, EPI> p)
 {
     using C = I8Cfg<NR>;
     constexpr int STAGES = C::kStages;
@@ -330,14 +327,21 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
                             v[j] += pre[j];
                     }
                     EpiOps ops[CG / 3];
-                    const float bias = i8_epi_ops<EPI, CG / 3>(p, pnl * kPanelRows + row, c0 / 3, M, ops);
+                    float bias = 0.f;
+                    if constexpr (EPI)
+                        bias = i8_epi_ops(p.epi, p.N, pnl * kPanelRows + row, c0 / 3, M, ops);
 #pragma unroll
                     for (int t = 0; t < CG / 3; ++t) {
                         const int m = c0 / 3 + t; // the same across the warp
                         if (m < M)
-                            imma_emit_rows<8, EPI>(p.x, p.wq, p.scales, nullptr, p.epi, p.y, K, KB, p.N, pnl * kPanelRows + 32 * quad,
-                                              m, i8_value(v[3 * t], v[3 * t + 1], v[3 * t + 2], s_n * pow2_of(-s_e[m])),
-                                              128.0 * s_n * s_rb[m], bias, ops[t], lane);
+                            imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
+                                              i8_value(v[3 * t], v[3 * t + 1], v[3 * t + 2], s_n * pow2_of(-s_e[m])),
+                                              128.0 * s_n * s_rb[m], lane, [&](int n, double y) {
+                                if constexpr (EPI)
+                                    epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[t]);
+                                else
+                                    p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
+                            });
                     }
                 } else {
 #pragma unroll
@@ -381,14 +385,21 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
                         tot[j] += v[j];
                 }
                 EpiOps ops[CG / 3];
-                const float bias = i8_epi_ops<EPI, CG / 3>(p, pnl * kPanelRows + row, c0 / 3, M, ops);
+                float bias = 0.f;
+                if constexpr (EPI)
+                    bias = i8_epi_ops(p.epi, p.N, pnl * kPanelRows + row, c0 / 3, M, ops);
 #pragma unroll
                 for (int t = 0; t < CG / 3; ++t) {
                     const int m = c0 / 3 + t; // the same across the warp
                     if (m < M)
-                        imma_emit_rows<8, EPI>(p.x, p.wq, p.scales, nullptr, p.epi, p.y, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
+                        imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
                                           i8_value(tot[3 * t], tot[3 * t + 1], tot[3 * t + 2], s_n * pow2_of(-s_e[m])),
-                                          128.0 * s_n * s_rb[m], bias, ops[t], lane);
+                                          128.0 * s_n * s_rb[m], lane, [&](int n, double y) {
+                            if constexpr (EPI)
+                                epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[t]);
+                            else
+                                p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
+                        });
                 }
             }
             if (lane == 0)
@@ -445,7 +456,7 @@ static cudaError_t launch_i8_e(const LinearArgs &a, void *ws, int sm_count, cuda
             return e;
     }
     const Shape sh{8, a.K, a.N, 0};
-    I8Params p;
+    EpiParams<I8Params, EPI> p;
     p.x = a.x;
     p.M = a.M;
     p.K = a.K;
@@ -455,7 +466,8 @@ static cudaError_t launch_i8_e(const LinearArgs &a, void *ws, int sm_count, cuda
     p.wq = (const uint8_t *)a.wq;
     p.scales = (const uint16_t *)a.scales;
     p.y = a.y;
-    p.epi = a.epi ? *a.epi : EpiArgs{};
+    if constexpr (EPI)
+        p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.grid = p.cnt + ws_grid_counter();
     p.res = reinterpret_cast<unsigned long long *>(p.cnt + ws_res_counter());

@@ -46,7 +46,6 @@ struct GemmSkParams {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
-    EpiArgs epi; // the EPI instances' epilogue
     float *part;   // [CTAs][2][128 rows][NT]
     uint32_t *cnt; // [panels][8]
 };
@@ -103,7 +102,7 @@ __device__ __forceinline__ void tmem_load_cols(uint32_t taddr, float (&v)[HALF])
 
 template <int BITS, int NT, bool EPI>
 __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kMaxRegs))
-    gemm_sk_kernel(const __grid_constant__ CUtensorMap tmx, const GemmSkParams p)
+    gemm_sk_kernel(const __grid_constant__ CUtensorMap tmx, const EpiParams<GemmSkParams, EPI> p)
 {
     using C = GskCfg<BITS, NT>;
     constexpr int STAGES = C::kStages, TCOLS = C::kTmemCols, A0 = C::kA0;
@@ -263,7 +262,15 @@ __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kM
             if constexpr (BITS == 8)
                 scale = nrow < p.N ? bf16_bits_to_float(p.scales[nrow]) : 0.f;
             auto store_y = [&](const float (&t)[HALF]) {
-                if (nrow < p.N) {
+                if constexpr (!EPI) {
+                    if (nrow < p.N) {
+#pragma unroll
+                        for (int c = 0; c < HALF; ++c)
+                            if (h * HALF + c < p.M)
+                                p.y[(size_t)(h * HALF + c) * p.N + nrow] =
+                                    __bfloat16_as_ushort(__float2bfloat16_rn(t[c] * scale));
+                    }
+                } else if (nrow < p.N) {
                     const float bias = epi_bias<EPI>(p.epi, nrow);
                     constexpr int B = HALF < 16 ? HALF : 16; // a batch's operands in flight together
 #pragma unroll
@@ -330,7 +337,15 @@ __global__ void __launch_bounds__(kGskThreads) __maxnreg__((GskCfg<BITS, NT>::kM
                         }
                     }
                 }
-                if (nrow < p.N) {
+                if constexpr (!EPI) {
+                    if (nrow < p.N) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c)
+                            if (h * HALF + c0 + c < p.M)
+                                p.y[(size_t)(h * HALF + c0 + c) * p.N + nrow] =
+                                    __bfloat16_as_ushort(__float2bfloat16_rn(tot[c] * scale));
+                    }
+                } else if (nrow < p.N) {
                     const float bias = epi_bias<EPI>(p.epi, nrow);
                     EpiOps o[CH];
                     epi_load_tokens<EPI>(p.epi, o, h * HALF + c0, p.M - h * HALF - c0, nrow);
@@ -490,7 +505,7 @@ static cudaError_t launch_gemm_sk_e(const LinearArgs &a, int ctas_per_sm, void *
     if (!make_x_map<NT>(&map, a.x, a.M, a.K))
         return cudaErrorInvalidValue;
     const Shape sh{a.bits, a.K, a.N, a.group};
-    GemmSkParams p;
+    EpiParams<GemmSkParams, EPI> p;
     p.M = a.M;
     p.K = a.K;
     p.N = a.N;
@@ -500,7 +515,8 @@ static cudaError_t launch_gemm_sk_e(const LinearArgs &a, int ctas_per_sm, void *
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
-    p.epi = a.epi ? *a.epi : EpiArgs{};
+    if constexpr (EPI)
+        p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.part = (float *)((uint8_t *)ws + ws_counter_bytes());
     const int per_sm = (ctas_per_sm >= 1 && ctas_per_sm < C::kOcc) ? ctas_per_sm : C::kOcc;

@@ -63,7 +63,6 @@ struct GemmW4Params {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
-    EpiArgs epi; // the EPI instances' epilogue
     float *part;   // [CTAs][2 slots][NT tokens][128 rows]
     uint32_t *cnt; // [panels][8] tickets
 };
@@ -140,8 +139,8 @@ constexpr size_t gemm_w4_smem_bytes()
 // whole: this CTA (cf = cl) had the panel to itself and its totals stand in its
 // second slot.
 template <int NT, int CW, bool EPI>
-__device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &sk, int pnl, int cf, int cl, int r,
-                                         int t0, bool whole = false)
+__device__ __forceinline__ void w4_fixup(const EpiParams<GemmW4Params, EPI> &p, const SkTable &sk, int pnl, int cf,
+                                         int cl, int r, int t0, bool whole = false)
 {
     const int nrow = pnl * kPanelRows + r;
     // With an epilogue 8 tokens at a time, the operands' loads beside the partials':
@@ -149,23 +148,24 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
     // spill at 64 tokens.
     constexpr int CG = 4, TB = EPI ? 8 : 16;
     float bias = 0.f;
-    if (nrow < p.N)
-        bias = epi_bias<EPI>(p.epi, nrow);
+    if constexpr (EPI)
+        if (nrow < p.N)
+            bias = epi_bias<true>(p.epi, nrow);
     for (int j0 = 0; j0 < CW; j0 += TB) {
-        const int jn = min(TB, p.M - t0 - j0);
         float acc[TB];
         EpiOps o[TB];
 #pragma unroll
         for (int j = 0; j < TB; ++j)
             acc[j] = 0.f;
-        epi_load_tokens<EPI>(p.epi, o, t0 + j0, nrow < p.N ? jn : 0, nrow);
+        if constexpr (EPI)
+            epi_load_tokens<true>(p.epi, o, t0 + j0, nrow < p.N ? p.M - t0 - j0 : 0, nrow);
         for (int c0 = cf; c0 <= cl; c0 += CG) {
             float v[CG][TB];
 #pragma unroll
             for (int u = 0; u < CG; ++u) {
                 const int cc = c0 + u;
                 if (cc <= cl) {
-                    const int sl = pnl == sk.first[cc] && !whole ? 0 : 1;
+                    const int sl = pnl == sk.first[cc] && !(EPI && whole) ? 0 : 1;
                     const float *src = p.part + ((size_t)(cc * 2 + sl) * NT + t0 + j0) * kPanelRows + r;
 #pragma unroll
                     for (int j = 0; j < TB; ++j)
@@ -179,26 +179,38 @@ __device__ __forceinline__ void w4_fixup(const GemmW4Params &p, const SkTable &s
                     for (int j = 0; j < TB; ++j)
                         acc[j] += v[u][j];
         }
-        EpiArgs rest = p.epi;
-        if (EPI && !p.epi.out_f32) {
+        if constexpr (EPI) {
+            const int jn = min(TB, p.M - t0 - j0);
+            EpiArgs rest = p.epi;
+            if (!p.epi.out_f32) {
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
-                acc[j] += bias;
-            epi_activations(acc, p.epi.act);
-            rest.act = WQ_ACT_NONE;
-        }
-        if (nrow < p.N) {
+                for (int j = 0; j < TB; ++j)
+                    acc[j] += bias;
+                epi_activations(acc, p.epi.act);
+                rest.act = WQ_ACT_NONE;
+            }
+            if (nrow < p.N) {
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
+                for (int j = 0; j < TB; ++j)
+                    if (j < jn)
+                        epi_store<true>(rest, p.y, p.N, t0 + j0 + j, nrow, acc[j], 0.f, o[j]);
+            }
+        } else if (nrow < p.N) {
+            const int jn = min(TB, p.M - t0 - j0);
+            uint16_t *yp = p.y + (size_t)(t0 + j0) * p.N + nrow;
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
                 if (j < jn)
-                    epi_store<EPI>(rest, p.y, p.N, t0 + j0 + j, nrow, acc[j], 0.f, o[j]);
+                    *yp = __bfloat16_as_ushort(__float2bfloat16_rn(acc[j]));
+                yp += p.N;
+            }
         }
     }
 }
 
 template <int NT, bool EPI>
 __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const __grid_constant__ CUtensorMap tmx,
-                                                                const __grid_constant__ GemmW4Params p)
+                                                                const EpiParams<GemmW4Params, EPI> p)
 {
     using C = W4Cfg<NT>;
     constexpr int XS = C::kXS, SS = C::kSS, AS = C::kAS, ACC = C::kACC, DEPTH = C::kDepth, SLOT = C::kSlot;
@@ -359,7 +371,13 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1) gemm_w4_kernel(const _
                     w4_fixup<NT, CW, true>(p, sk, pnl, cta, cta, r, t0, true); // each thread reads what it wrote
                 } else if (nrow < p.N) {
                     const int jn = min(CW, p.M - t0); // tokens of this slice that exist
-                    epi_store_tokens<false, CW>(p.epi, p.y, p.N, t0, jn, nrow, tot);
+                    uint16_t *yp = p.y + (size_t)t0 * p.N + nrow;
+#pragma unroll
+                    for (int j = 0; j < CW; ++j) {
+                        if (j < jn)
+                            *yp = __bfloat16_as_ushort(__float2bfloat16_rn(tot[j]));
+                        yp += p.N;
+                    }
                 }
                 return;
             }
@@ -528,7 +546,7 @@ static cudaError_t launch_gemm_w4_e(const LinearArgs &a, void *ws, int sm_count,
     if (!make_x_map<NT>(&map, a.x, a.M, a.K))
         return cudaErrorInvalidValue;
     const Shape sh{a.bits, a.K, a.N, a.group};
-    GemmW4Params p;
+    EpiParams<GemmW4Params, EPI> p;
     p.M = a.M;
     p.K = a.K;
     p.N = a.N;
@@ -538,7 +556,8 @@ static cudaError_t launch_gemm_w4_e(const LinearArgs &a, void *ws, int sm_count,
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
-    p.epi = a.epi ? *a.epi : EpiArgs{};
+    if constexpr (EPI)
+        p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.part = (float *)((uint8_t *)ws + ws_counter_bytes());
     int G = sm_count;

@@ -61,7 +61,6 @@ struct GiParams {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
-    EpiArgs epi; // the EPI instances' epilogue
     uint32_t *part; // [kGiMaxWarps][2 slots][16 rows][NR] partials
     uint32_t *cnt;  // one ticket per 16-row block
     const uint32_t *wmax; // INT4: max |s (q - z)| over the whole weight (binary32 bits, packed trailer)
@@ -314,8 +313,8 @@ __host__ __device__ __forceinline__ bool gi_contrib_at(const GiParams &p, int G,
 // n0 + r): value(q) is the integer path's y in binary64.  The exactness
 // guard (wq_imma.cuh) vouches for it or the warp recomputes that output in
 // binary64 from x and the packed codes.  All 32 lanes call it together.
-template <int BITS, bool EPI, class Value>
-__device__ __forceinline__ void gi_emit(const GiParams &p, int n0, const int *s_e, const unsigned long long *s_res,
+template <int BITS, bool EPI, class Params, class Value>
+__device__ __forceinline__ void gi_emit(const Params &p, int n0, const int *s_e, const unsigned long long *s_res,
                                         Value value, int lane)
 {
     const int M = p.M, N = p.N;
@@ -326,22 +325,32 @@ __device__ __forceinline__ void gi_emit(const GiParams &p, int n0, const int *s_
         float bias = 0.f;
         EpiOps o = epi_none();
         if (q < 16 * M) {
-            o = epi_load<EPI>(p.epi, m, n0 + r);
-            bias = epi_bias<EPI>(p.epi, n0 + r);
+            if constexpr (EPI) {
+                o = epi_load<true>(p.epi, m, n0 + r);
+                bias = epi_bias<true>(p.epi, n0 + r);
+            }
             const double v = value(q);
             const double wmax =
                 BITS == 8 ? 128.0 * (double)bf16_bits_to_float(p.scales[n0 + r]) : (double)wmax4;
             redo = !exact_enough(v, wmax * residual_bound(s_res[m], s_e[m]));
-            if (!redo)
-                epi_store64<EPI>(p.epi, p.y, N, m, n0 + r, v, bias, o);
+            if (!redo) {
+                if constexpr (EPI)
+                    epi_store64<true>(p.epi, p.y, N, m, n0 + r, v, bias, o);
+                else
+                    p.y[(size_t)m * N + n0 + r] = __bfloat16_as_ushort(__double2bfloat16(v));
+            }
         }
         for (uint32_t mask = __ballot_sync(0xffffffffu, redo); mask; mask &= mask - 1) {
             const int src = __ffs(mask) - 1, qq = q0 + src, rr = qq & 15, mm = qq >> 4;
             double v = packed_row_dot<BITS>(p.wq, p.scales, p.zeros, p.K, p.KB, n0 + rr, p.x + (size_t)mm * p.K, lane);
             if constexpr (BITS == 8)
                 v *= (double)bf16_bits_to_float(p.scales[n0 + rr]);
-            if (lane == src)
-                epi_store64<EPI>(p.epi, p.y, N, mm, n0 + rr, v, bias, o);
+            if (lane == src) {
+                if constexpr (EPI)
+                    epi_store64<true>(p.epi, p.y, N, mm, n0 + rr, v, bias, o);
+                else
+                    p.y[(size_t)mm * N + n0 + rr] = __bfloat16_as_ushort(__double2bfloat16(v));
+            }
         }
     }
 }
@@ -349,7 +358,7 @@ __device__ __forceinline__ void gi_emit(const GiParams &p, int n0, const int *s_
 // One segment's output, its accumulators in red ([16 rows][NR]; INT8 int32
 // digit sums D_i, INT4 fp32 group-scaled sums A_i): y of the 16 x M outputs.
 template <int BITS, int NR, bool EPI>
-__device__ __forceinline__ void gi_write_y(const GiParams &p, int rb, const uint32_t *red, const int *s_e,
+__device__ __forceinline__ void gi_write_y(const EpiParams<GiParams, EPI> &p, int rb, const uint32_t *red, const int *s_e,
                                            const unsigned long long *s_res, int lane)
 {
     const int n0 = 16 * rb;
@@ -404,7 +413,7 @@ __device__ __forceinline__ uint32_t gi_shared_partial(const GiParams &p, int rb,
 // Its ticket's acquire (taken earlier in program order) orders the reads.
 // list: this warp's scratch of at least CPR words (partial offsets).
 template <int BITS, int NT, int WARPS, bool EPI>
-__device__ __forceinline__ void gi_shared_fixup(const GiParams &p, int rb, uint32_t ticket, int G, const int *s_e,
+__device__ __forceinline__ void gi_shared_fixup(const EpiParams<GiParams, EPI> &p, int rb, uint32_t ticket, int G, const int *s_e,
                                                 const unsigned long long *s_res, uint32_t *list, int lane)
 {
     constexpr int NR = 8 * NT;
@@ -483,7 +492,7 @@ __device__ __forceinline__ void gi_shared_fixup(const GiParams &p, int rb, uint3
 // order (INT8: exact integers; INT4: each contributor's value in binary64,
 // summed in binary64) and written to y.
 template <int BITS, int NT, int WARPS, bool EPI>
-__device__ __forceinline__ void gi_local_out(const GiParams &p, const GiCta &ct, int c, const uint32_t *stash,
+__device__ __forceinline__ void gi_local_out(const EpiParams<GiParams, EPI> &p, const GiCta &ct, int c, const uint32_t *stash,
                                              const int *s_e, const unsigned long long *s_res, int warp, int lane)
 {
     constexpr int NR = 8 * NT;
@@ -525,7 +534,7 @@ __device__ __forceinline__ void gi_local_out(const GiParams &p, const GiCta &ct,
 // WARPS = 16: one CTA per SM (the digit rows made once per SM); WARPS = 8:
 // two per SM.  Either way 128 registers per thread and 16 warps per SM.
 template <int BITS, int NT, int WARPS, bool EPI>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_i8_kernel(const GiParams p)
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_i8_kernel(const EpiParams<GiParams, EPI> p)
 {
     constexpr int NR = 8 * NT;
     constexpr int D = GiCfg<BITS>::D;
@@ -842,7 +851,7 @@ static cudaError_t launch_gi_t(const LinearArgs &a, void *ws, int sm_count, cuda
     }
     const int per_sm = occ < 16 / WARPS ? occ : 16 / WARPS;
     const Shape sh{a.bits, a.K, a.N, a.group};
-    GiParams p;
+    EpiParams<GiParams, EPI> p;
     p.x = a.x;
     p.M = a.M;
     p.K = a.K;
@@ -854,7 +863,8 @@ static cudaError_t launch_gi_t(const LinearArgs &a, void *ws, int sm_count, cuda
     p.scales = (const uint16_t *)a.scales;
     p.zeros = (const uint8_t *)a.zeros;
     p.y = a.y;
-    p.epi = a.epi ? *a.epi : EpiArgs{};
+    if constexpr (EPI)
+        p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.part = (uint32_t *)((uint8_t *)ws + ws_counter_bytes());
     p.wmax = trailer_wmax(a.wq, sh);

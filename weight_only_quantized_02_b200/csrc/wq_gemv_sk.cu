@@ -38,7 +38,6 @@ struct GemvSkParams {
     const uint16_t *scales;
     const uint8_t *zeros;
     uint16_t *y;
-    EpiArgs epi; // the EPI instances' epilogue
     int KB, U; // k-blocks per panel, units = panels * KB
     float *part;
     uint32_t *cnt;
@@ -146,7 +145,7 @@ __device__ __forceinline__ void sk_int4_tile(const uint4 &w, const uint8_t *xs, 
 
 // OCC = CTAs per SM the instance is built for (register bound and ring depth).
 template <int BITS, int MT, int OCC, bool EPI>
-__global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const GemvSkParams p)
+__global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const EpiParams<GemvSkParams, EPI> p)
 {
     using C = SkCfg<BITS, MT, OCC>;
     constexpr int STAGES = C::kStages;
@@ -247,26 +246,44 @@ __global__ void __launch_bounds__(kSkThreads, OCC) gemv_sk_kernel(const GemvSkPa
                 s_hi = n_hi < p.N ? bf16_bits_to_float(p.scales[n_hi]) : 0.f;
             }
             auto store_y = [&](const float (&v)[MT][4]) {
-                const float b_lo = n_lo < p.N ? epi_bias<EPI>(p.epi, n_lo) : 0.f;
-                const float b_hi = n_hi < p.N ? epi_bias<EPI>(p.epi, n_hi) : 0.f;
-                EpiOps o[4 * MT]; // every operand in flight together
-                epi_load_batch<EPI>(p.epi, o, [&](int j, int &m, int &n) {
-                    m = 8 * (j / 4) + 2 * t + j / 2 % 2;
-                    n = j % 2 ? n_hi : n_lo;
-                    return m < p.M && n < p.N;
-                });
+                if constexpr (!EPI) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const int m0 = 8 * mt + 2 * t;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int m = 8 * mt + 2 * t + e;
-                        if (m < p.M) {
-                            if (n_lo < p.N)
-                                epi_store<EPI>(p.epi, p.y, p.N, m, n_lo, v[mt][e] * s_lo, b_lo, o[4 * mt + 2 * e]);
-                            if (n_hi < p.N)
-                                epi_store<EPI>(p.epi, p.y, p.N, m, n_hi, v[mt][2 + e] * s_hi, b_hi, o[4 * mt + 2 * e + 1]);
+                        for (int e = 0; e < 2; ++e) {
+                            if (m0 + e < p.M) {
+                                if (n_lo < p.N)
+                                    p.y[(size_t)(m0 + e) * p.N + n_lo] =
+                                        __bfloat16_as_ushort(__float2bfloat16_rn(v[mt][e] * s_lo));
+                                if (n_hi < p.N)
+                                    p.y[(size_t)(m0 + e) * p.N + n_hi] =
+                                        __bfloat16_as_ushort(__float2bfloat16_rn(v[mt][2 + e] * s_hi));
+                            }
                         }
                     }
+                } else {
+                    const float b_lo = n_lo < p.N ? epi_bias<EPI>(p.epi, n_lo) : 0.f;
+                    const float b_hi = n_hi < p.N ? epi_bias<EPI>(p.epi, n_hi) : 0.f;
+                    EpiOps o[4 * MT]; // every operand in flight together
+                    epi_load_batch<EPI>(p.epi, o, [&](int j, int &m, int &n) {
+                        m = 8 * (j / 4) + 2 * t + j / 2 % 2;
+                        n = j % 2 ? n_hi : n_lo;
+                        return m < p.M && n < p.N;
+                    });
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int m = 8 * mt + 2 * t + e;
+                            if (m < p.M) {
+                                if (n_lo < p.N)
+                                    epi_store<EPI>(p.epi, p.y, p.N, m, n_lo, v[mt][e] * s_lo, b_lo, o[4 * mt + 2 * e]);
+                                if (n_hi < p.N)
+                                    epi_store<EPI>(p.epi, p.y, p.N, m, n_hi, v[mt][2 + e] * s_hi, b_hi, o[4 * mt + 2 * e + 1]);
+                            }
+                        }
+                }
             };
             if (lo == pnl * KB && hi == (pnl + 1) * KB) {
                 store_y(acc);
@@ -424,7 +441,7 @@ static cudaError_t launch_sk_t(const LinearArgs &a, void *ws, int sm_count, cuda
     }
     const int per_sm = OCC < occ ? OCC : occ; // every CTA resident at once
     const Shape sh{a.bits, a.K, a.N, a.group};
-    GemvSkParams p;
+    EpiParams<GemvSkParams, EPI> p;
     p.x = a.x;
     p.M = a.M;
     p.K = a.K;
@@ -435,7 +452,8 @@ static cudaError_t launch_sk_t(const LinearArgs &a, void *ws, int sm_count, cuda
     p.y = a.y;
     p.KB = sh.kblocks();
     p.U = sh.panels() * sh.kblocks();
-    p.epi = a.epi ? *a.epi : EpiArgs{};
+    if constexpr (EPI)
+        p.epi = *a.epi;
     p.cnt = (uint32_t *)ws;
     p.part = (float *)((uint8_t *)ws + ws_counter_bytes());
     int G = per_sm * sm_count;
@@ -558,7 +576,6 @@ static cudaError_t launch_sk_noalloc_t(const LinearArgs &a, uint32_t *cnt, float
     p.y = a.y;
     p.KB = sh.kblocks();
     p.U = sh.panels() * sh.kblocks();
-    p.epi = EpiArgs{};
     p.cnt = cnt;
     p.part = part;
     int G = per_sm * sm_count;

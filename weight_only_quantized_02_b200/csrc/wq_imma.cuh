@@ -235,28 +235,27 @@ __device__ __noinline__ double packed_row_dot(const uint8_t *__restrict__ wq, co
     return acc;
 }
 
-// Writes y[m][n] from v, through the epilogue (bias and o: this lane's
-// operands), for the warp's 32 consecutive weight rows n = nb + lane
-// (token m the same across the warp; rows at or past N write nothing).  An
+// store(n, v) for the warp's 32 consecutive weight rows n = nb + lane
+// (token m the same across the warp; none for rows at or past N).  An
 // output whose bound the exactness guard cannot accept is recomputed by the
 // whole warp in binary64 (packed_row_dot; INT8 times s[n]).
-template <int BITS, bool EPI>
+template <int BITS, class Store>
 __device__ __forceinline__ void imma_emit_rows(const uint16_t *__restrict__ x, const uint8_t *__restrict__ wq,
                                                const uint16_t *__restrict__ scales, const uint8_t *__restrict__ zeros,
-                                               const EpiArgs &epi, uint16_t *y, int K, int KB, int N, int nb, int m,
-                                               double v, double bound, float bias, const EpiOps &o, int lane)
+                                               int K, int KB, int N, int nb, int m, double v, double bound, int lane,
+                                               Store store)
 {
     const int n = nb + lane;
     const bool redo = n < N && !exact_enough(v, bound);
     if (n < N && !redo)
-        epi_store64<EPI>(epi, y, N, m, n, v, bias, o);
+        store(n, v);
     for (uint32_t mask = __ballot_sync(0xffffffffu, redo); mask; mask &= mask - 1) {
         const int src = __ffs(mask) - 1, nn = nb + src;
         double r = packed_row_dot<BITS>(wq, scales, zeros, K, KB, nn, x + (size_t)m * K, lane);
         if constexpr (BITS == 8)
             r *= (double)bf16_bits_to_float(scales[nn]);
         if (lane == src)
-            epi_store64<EPI>(epi, y, N, m, nn, r, bias, o);
+            store(nn, r);
     }
 }
 
