@@ -31,11 +31,12 @@
 
 namespace wq {
 
-// A kernel's parameters, with an epilogue or without.  The instances without one
-// have nothing of it, parameters and stores included, so that they are compiled as
-// if there were none: with it among the parameters, and stores shared by both forms,
-// the integer GEMV of 5120 x 17408 took 21.6 us at four tokens instead of 19.9, the
-// role-split GEMM of 17408 x 5120 33.9 at 64 instead of 32.3.
+// A kernel's parameters, with an epilogue or without.  The stream-K, integer and
+// role-split kernels' instances without one have nothing of it, parameters and stores
+// included, so that they are compiled as if there were none: with it among the
+// parameters, and stores shared by both forms, the integer GEMV of 5120 x 17408 took
+// 21.6 us at four tokens instead of 19.9, the role-split GEMM of 17408 x 5120 33.9 at
+// 64 instead of 32.3.  (The other two kernels' stores are shared and cost the same.)
 template <class Params>
 struct WithEpilogue : Params {
     EpiArgs epi;
