@@ -477,3 +477,20 @@ def test_activations_over_their_range(bits, group, M, dtype, act):
     ends = [0.0 if act != "none" else -torch.finfo(dtype).max, torch.finfo(dtype).max]
     assert torch.equal(y[:, :2].double(), torch.tensor([ends] * M, dtype=torch.float64, device=dev()))
     check(y[:, 2:], x, w[2:], bias[2:], act, None, None, dtype)
+
+
+@pytest.mark.parametrize("bits,group,K,N,M", [(8, 0, 32, 1 << 20, 130), (4, 128, 128, 1 << 20, 3), (8, 0, 32, 16, 65536),
+                                              (4, 128, 128, 16, 65536), (4, 64, 128, 16, 65536)])
+def test_largest_sizes(bits, group, K, N, M):
+    """The most output channels and the most tokens; the corners are looked at, and
+    the rows around y stay as they were."""
+    pw, w = make_weight(bits, group, K, N)
+    x, bias, mul, res = operands(M, K, N, torch.bfloat16)
+    buf = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=dev())
+    y = wq.wq_linear_epilogue(x, pw, bias=bias, act=wq.WQ_ACT_SILU, mul=mul, residual=res, ws=ws_for(128, K, N),
+                              y=buf[1:M + 1])
+    for n in (slice(0, 300), slice(max(0, N - 300), N)):
+        for m in (slice(0, 300), slice(max(0, M - 300), M)):
+            check(y[m, n], x[m], w[n], bias[n], "silu", mul[m, n], res[m, n], torch.bfloat16)
+    assert bool((buf[0] == 7).all()) and bool((buf[M + 1] == 7).all())
+    assert wq.wq_device_error() == 0
