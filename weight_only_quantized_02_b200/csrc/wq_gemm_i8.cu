@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
 #pragma unroll
             for (int c0 = 0; c0 < NR; c0 += CG) {
                 int32_t v[CG];
+                __syncwarp(); // the last pass's stores branch by lane; the load is the whole warp's
 #pragma unroll
                 for (int cc = 0; cc < CG; cc += 8) {
                     float f[8];

@@ -140,7 +140,8 @@ __device__ __forceinline__ uint32_t pf_map(const void *p, uint32_t rank)
 // took 1400 cycles.
 // One lane's (who) arrival for its warp, by predicate: the tensor-memory
 // instructions around it are the whole warp's, and a branch could leave the warp
-// split on the way to the next of them.
+// split on the way to the next of them.  (Where code branches by lane on that way,
+// a __syncwarp or a vote stands before the next one.)
 __device__ __forceinline__ void pf_arrive(uint32_t cluster_bar, bool who)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
@@ -460,6 +461,9 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
         out.fetch(0);
     for (int i = 0; i < chunks; ++i) {
         float v[16];
+        // The operands and the last chunk's stores branch by lane (ragged N and M): the
+        // warp has to be whole again for the tensor-memory load.
+        __syncwarp();
         tmem_ld_32x32b_x16(tq + 16 * i + (i >= nc ? kPfTok - 16 * nc : 0), v);
         tmem_wait_ld();
         if (i == chunks - 1) {
@@ -484,8 +488,10 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
         __syncwarp();
         pf_arrive(rt.ebar + b * 8, lane == 0);
     }
-    if (whole)
+    if (whole) {
+        __syncwarp();
         return;
+    }
     const int cf = pf_owner(p, rt.G, tile * KB), cl = pf_owner(p, rt.G, (tile + 1) * KB - 1);
     uint32_t *counter = p.cnt + (cf * 2 + rt.rank) * PfCfg<BITS>::kGroups + out.id - 1;
     __threadfence();
@@ -530,6 +536,7 @@ __device__ __noinline__ void pf_flush(const PfParams &p, const PfRetire &rt, int
     }
     if (out.r == 0)
         atomicExch(counter, 0u); // ready for the next call
+    __syncwarp(); // the caller's next tensor-memory instruction is the whole warp's
 }
 
 template <int BITS, bool F16>
