@@ -56,7 +56,8 @@
 // warps a scheduler; neither alone (a third of the retirement 320 us, no conversion
 // of the codes 327).
 //
-// Every wait is bounded (2 s); a timeout is recorded and every role winds down.
+// Every wait is bounded (2 s); a timeout is recorded, every role winds down, and the
+// producers wait (as long at most) for their copies in flight before the CTAs leave.
 #include <atomic>
 #include <cstdint>
 
@@ -604,7 +605,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
             const int half = p.n >> 1, tx = p.nsub * p.n * 128; // tx: both CTAs' bytes
             const uint32_t bar = pf_map(xfull, 0);
             int kb = kb0, tt = tile0 % p.TT;
-            for (int i = 0; i < 2 * nu; ++i) {
+            int i = 0;
+            for (; i < 2 * nu; ++i) {
                 const int xs = i % XS;
                 if (i >= XS && !mbar_wait(&done[xs], ((i / XS) - 1) & 1)) {
                     ok = false;
@@ -621,13 +623,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                         tt = 0;
                 }
             }
+            // Neither CTA leaves with a copy in flight, not after a wait that gave up
+            // either: the leader's barriers count both CTAs' bytes.
+            if (rank == 0)
+                for (int j = max(0, i - XS); j < i; ++j)
+                    if (!mbar_wait(&xfull[j % XS], (j / XS) & 1)) {
+                        ok = false;
+                        break;
+                    }
         } else if (warp == 1 && lane == 0) {
             // ---------------- weight producer ----------------
             const uint64_t pol = policy_evict_first();
             int kb = kb0, tt = tile0 % p.TT, pnl = 2 * (tile0 / p.TT) + (int)rank;
             int ws = 0;
             uint32_t wpar = 1; // the stage's last round; its first needs no wait
-            for (int i = 0; i < nu; ++i) {
+            int i = 0;
+            for (; i < nu; ++i) {
                 if (i >= WS && !mbar_wait(&wempty[ws], wpar)) {
                     ok = false;
                     break;
@@ -653,6 +664,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                     }
                 }
             }
+            for (int j = max(0, i - WS); j < i; ++j) // as the x producer's
+                if (!mbar_wait(&wfull[j % WS], (j / WS) & 1)) {
+                    ok = false;
+                    break;
+                }
         } else if (warp == 2 && rank == 0) {
             // ---------------- MMA issuer ----------------
             // The whole warp walks the steps, so that addresses and descriptors
