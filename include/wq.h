@@ -247,9 +247,13 @@ typedef struct {
 
 /* The layer with its epilogue in the same kernel:
  *     y = act(x . dequant(Wq)^T + bias) * mul + residual
- * x, y bf16; the epilogue in fp32 on the fp32-accumulated sum (the integer
- * paths' binary64 sum), rounded once.  The operands need element alignment
- * only.  y may be the residual or mul buffer itself (same address, row stride
+ * x, y bf16; the epilogue in fp32 on the fp32-accumulated sum v (the integer
+ * paths' binary64 sum), rounded once.  The integer paths' sum is that of x held to
+ * 22 bits below the row's largest, or the exact one where that could be further
+ * off than 2^-9 max(|v|, 1), as for wq_linear; with mul, than the larger of
+ * 2^-9 |v| and max(4, K / 1024) 2^-21 max|x[m]| w, w the largest |weight| that the
+ * codes can stand for (of the channel for INT8, of all for INT4).  The operands
+ * need element alignment only.  y may be the residual or mul buffer itself (same address, row stride
  * N: the residual stream updated in place); it must not overlap them, or x,
  * in any other way.
  *   epilogue  host, required; with every part absent y is the layer, rounded
@@ -358,7 +362,11 @@ int wq_logprobs(const void *logits, int dtype, int M, int N, int64_t ld, const i
                 cudaStream_t stream);
 
 /* wq_logprobs of the logits x . dequant(Wq)^T of a quantized vocabulary head,
- * which are formed in fp32 and never rounded to 16 bits or returned.
+ * which are formed in fp32 and never rounded to 16 bits or returned.  The integer
+ * paths' logits are off by the larger of 2^-21 |logit| and max(4, K / 1024) 2^-21
+ * max|x[m]| w at most (w as in wq_linear_epilogue), fp32 roundings aside; the logits
+ * of a row with an element some 2^7 times the others' size are mostly formed again in
+ * binary64, which takes longer.
  *   scratch   device, at least wq_linear_logprobs_workspace_bytes(M, N) bytes,
  *             16-byte aligned, owned by the caller: the fp32 logits of up to
  *             512 tokens at a time, in turn

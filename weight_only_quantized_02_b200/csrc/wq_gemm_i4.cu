@@ -352,7 +352,8 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p
         const int et = threadIdx.x - 64; // 0..127
         const int quad = warp & 3;
         imma_digit_phase<NR, true>(p.x, M, p.K, KB, c, G, et, p.xd, s_amax, s_e, p.grid, p.res);
-        ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb) && ok;
+        const auto tol = guard_tol<EPI>(p);
+        ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb, tol) && ok;
         const double wmax = (double)__uint_as_float(__ldg(p.wmax));
 
         // ---------------- epilogue: one thread per output channel ----------------
@@ -413,7 +414,7 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p
                             if (m < M) // the same across the warp
                                 imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.K, KB, p.N,
                                                   pnl * kPanelRows + 32 * quad, m, (double)acc[m] * pow2_of(-s_e[m]),
-                                                  wmax * s_rb[m], lane, [&](int n, double y) {
+                                                  wmax * s_rb[m], tol, lane, [&](int n, double y) {
                                     if constexpr (EPI)
                                         epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[m]);
                                     else
@@ -460,7 +461,7 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p
                         if (m < M) // the same across the warp
                             imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.K, KB, p.N,
                                               pnl * kPanelRows + 32 * quad, m, (double)tot[m] * pow2_of(-s_e[m]),
-                                              wmax * s_rb[m], lane, [&](int n, double y) {
+                                              wmax * s_rb[m], tol, lane, [&](int n, double y) {
                                 if constexpr (EPI)
                                     epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[m]);
                                 else

@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
         const int K = p.K;
         // ---------------- activations: row maxima, then 1/G of the digit blocks ----------------
         imma_digit_phase<NR>(p.x, M, K, KB, c, G, et, p.xd, s_amax, s_e, p.grid, p.res);
-        ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb) && ok;
+        const auto tol = guard_tol<EPI>(p);
+        ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb, tol) && ok;
         // ---------------- epilogue: one thread per output channel ----------------
         const int row = 32 * quad + lane;
         const uint32_t tq = (uint32_t)(32 * quad) << 16;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
                         if (m < M)
                             imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
                                               i8_value(v[3 * t], v[3 * t + 1], v[3 * t + 2], s_n * pow2_of(-s_e[m])),
-                                              128.0 * s_n * s_rb[m], lane, [&](int n, double y) {
+                                              128.0 * s_n * s_rb[m], tol, lane, [&](int n, double y) {
                                 if constexpr (EPI)
                                     epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[t]);
                                 else
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
                     if (m < M)
                         imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
                                           i8_value(tot[3 * t], tot[3 * t + 1], tot[3 * t + 2], s_n * pow2_of(-s_e[m])),
-                                          128.0 * s_n * s_rb[m], lane, [&](int n, double y) {
+                                          128.0 * s_n * s_rb[m], tol, lane, [&](int n, double y) {
                             if constexpr (EPI)
                                 epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[t]);
                             else

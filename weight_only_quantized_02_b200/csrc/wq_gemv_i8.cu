@@ -319,6 +319,7 @@ __device__ __forceinline__ void gi_emit(const Params &p, int n0, const int *s_e,
 {
     const int M = p.M, N = p.N;
     const float wmax4 = BITS == 4 ? __uint_as_float(__ldg(p.wmax)) : 0.f;
+    const auto tol = guard_tol<EPI>(p);
     for (int q0 = 0; q0 < 16 * M; q0 += 32) {
         const int q = q0 + lane, r = q & 15, m = q >> 4;
         bool redo = false;
@@ -332,7 +333,7 @@ __device__ __forceinline__ void gi_emit(const Params &p, int n0, const int *s_e,
             const double v = value(q);
             const double wmax =
                 BITS == 8 ? 128.0 * (double)bf16_bits_to_float(p.scales[n0 + r]) : (double)wmax4;
-            redo = !exact_enough(v, wmax * residual_bound(s_res[m], s_e[m]));
+            redo = !tol(v, wmax * row_bound(s_res[m], s_e[m], tol));
             if (!redo) {
                 if constexpr (EPI)
                     epi_store64<true>(p.epi, p.y, N, m, n0 + r, v, bias, o);

@@ -129,6 +129,9 @@ __device__ __forceinline__ void digit_planes(const uint32_t (&w)[8], float s, ui
 // dynamic range never takes the binary64 path; a row holding elements far
 // below its largest (an outlier 2^12 above the rest) can take it for many
 // outputs, which is slow but exact.
+//
+// That tolerance belongs to a sum that is rounded to bf16 next.  An epilogue that
+// multiplies the sum, or hands it on in fp32, has its own (EpiTol).
 // ---------------------------------------------------------------------------
 constexpr double kExactTol = 1.0 / 512.0;
 
@@ -167,6 +170,53 @@ __device__ __forceinline__ double residual_bound(unsigned long long units, int e
 __device__ __forceinline__ bool exact_enough(double y, double bound)
 {
     return bound <= kExactTol * fmax(fabs(y), 1.0); // false for NaN: recomputed
+}
+
+// What the guard accepts of an output with value y and error bound `bound`.
+struct PlainTol {
+    static constexpr unsigned long long few = 0;
+    __device__ __forceinline__ bool operator()(double y, double bound) const { return exact_enough(y, bound); }
+};
+
+// With an epilogue: as above where act(y + bias) + residual follows; where the
+// result is multiplied, 2^-9 |y| alone (an absolute error of 2^-9 would be multiplied
+// as well); where y itself goes out in fp32, 2^-21 |y|.  Beside these two, rows
+// of which hardly anything was rounded are accepted whatever y is: R_m <= few, so
+// that y is off by at most few 2^-e max|w| <= few 2^-21 max|x| max|w|.  Without that
+// the outputs near zero of every row would be recomputed.  few = max(4, K / 1024):
+// a row of K normally distributed values has R_m around K / 20000, and stays below it
+// with a largest element up to some 2^6 times the others' size.  (Not for rows
+// whose exponent is held at 127, where 2^-e is more than 2^-21 of the largest.)
+struct EpiTol {
+    double rel, least;
+    unsigned long long few; // units of 2^-24
+    __device__ __forceinline__ EpiTol(const EpiArgs &e, int K)
+    {
+        const bool strict = e.out_f32 || e.mul;
+        rel = e.out_f32 ? 1.0 / 2097152.0 : kExactTol;
+        least = strict ? 0.0 : kExactTol;
+        few = strict ? (unsigned long long)max(4, K >> 10) << 24 : 0ull;
+    }
+    __device__ __forceinline__ bool operator()(double y, double bound) const
+    {
+        return bound <= fmax(rel * fabs(y), least); // false for NaN: recomputed
+    }
+};
+
+template <bool EPI, class Params>
+__device__ __forceinline__ auto guard_tol(const Params &p)
+{
+    if constexpr (EPI)
+        return EpiTol(p.epi, p.K);
+    else
+        return PlainTol();
+}
+
+// residual_bound, or 0 for a row that is accepted as it is.
+template <class Tol>
+__device__ __forceinline__ double row_bound(unsigned long long units, int e_m, const Tol &tol)
+{
+    return units <= tol.few && e_m < 127 ? 0.0 : residual_bound(units, e_m);
 }
 
 // Binary64 dot product of token row xm (bf16, K elements) with packed weight
@@ -239,14 +289,14 @@ __device__ __noinline__ double packed_row_dot(const uint8_t *__restrict__ wq, co
 // (token m the same across the warp; none for rows at or past N).  An
 // output whose bound the exactness guard cannot accept is recomputed by the
 // whole warp in binary64 (packed_row_dot; INT8 times s[n]).
-template <int BITS, class Store>
+template <int BITS, class Tol, class Store>
 __device__ __forceinline__ void imma_emit_rows(const uint16_t *__restrict__ x, const uint8_t *__restrict__ wq,
                                                const uint16_t *__restrict__ scales, const uint8_t *__restrict__ zeros,
-                                               int K, int KB, int N, int nb, int m, double v, double bound, int lane,
-                                               Store store)
+                                               int K, int KB, int N, int nb, int m, double v, double bound,
+                                               const Tol &tol, int lane, Store store)
 {
     const int n = nb + lane;
-    const bool redo = n < N && !exact_enough(v, bound);
+    const bool redo = n < N && !tol(v, bound);
     if (n < N && !redo)
         store(n, v);
     for (uint32_t mask = __ballot_sync(0xffffffffu, redo); mask; mask &= mask - 1) {
@@ -438,9 +488,11 @@ __device__ __forceinline__ void imma_digit_phase(const uint16_t *__restrict__ x,
 
 // After the digit phase, by the same 128 threads: once every CTA has counted
 // itself on grid[0] (acquire, bounded), the residual bound of every token row
-// into s_rb (residual_bound of the grid-wide sum).  False if the wait gave up.
+// into s_rb (row_bound of the grid-wide sum).  False if the wait gave up.
+template <class Tol>
 __device__ __forceinline__ bool imma_residual_bounds(int M, int G, int et, const uint32_t *grid,
-                                                     const unsigned long long *g_res, const int *s_e, double *s_rb)
+                                                     const unsigned long long *g_res, const int *s_e, double *s_rb,
+                                                     const Tol &tol)
 {
     bool ok = true;
     if (et < M) {
@@ -451,7 +503,7 @@ __device__ __forceinline__ bool imma_residual_bounds(int M, int G, int et, const
                 break;
             }
         }
-        s_rb[et] = ok ? residual_bound(__ldcg(g_res + et), s_e[et]) : 0.0;
+        s_rb[et] = ok ? row_bound(__ldcg(g_res + et), s_e[et], tol) : 0.0;
     }
     named_barrier_sync(1, 128);
     return ok;
