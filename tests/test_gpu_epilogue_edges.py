@@ -159,3 +159,38 @@ def test_fp32_logits_of_tiny_rows(bits, variant, M):
     # as above; fp32's own roundings of values around 2^-120 are its subnormals' step, 2^-149
     tol = (2.0 ** -21 + 2.0 ** -23) * v.abs() + 2.0 ** -149
     assert bool(((logits - v).abs() <= tol).all()), float(((logits - v).abs() / tol).max())
+
+
+# ---------------------------------------------------------------------------
+# activations that are not finite
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits,variant,split,M", [(8, 0, 3, 5), (8, 2, 4, 5), (8, 4, 1, 5), (8, 4, 1, 40), (8, 5, 1, 5),
+                                                  (8, 5, 2, 3), (8, None, 0, 200), (4, 0, 3, 5), (4, 2, 4, 5),
+                                                  (4, 4, 1, 20), (4, 5, 1, 5), (4, 6, 1, 40), (4, None, 0, 200)])
+def test_infinities_and_nan_in_a_row(bits, variant, split, M):
+    """A token with a NaN or an infinity has the outputs of binary64 arithmetic: NaN,
+    or an infinity of the weight's sign.  The other tokens' outputs are as without it."""
+    K, N = 640, 272
+    group = 128 if bits == 4 else 0
+    pw, w = make_weight(bits, group, K, N)
+    x, bias, _, res = operands(M, K, N, torch.bfloat16, 0, True, False, True)
+    if variant is not None:
+        wq.wq_set_choice(M, K, N, bits, group, variant, split)
+    clean = wq.wq_linear_epilogue(x, pw, bias=bias, residual=res, ws=ws_for(M, K, N))
+    check(clean, x, w, bias, "none", None, res, torch.bfloat16)
+    x[0, 3] = math.nan
+    x[1, 600] = math.inf
+    x[2, 0] = -math.inf
+    y = wq.wq_linear_epilogue(x, pw, bias=bias, residual=res, ws=ws_for(M, K, N))
+    assert torch.equal(y[3:], clean[3:])
+    assert bool(y[0].isnan().all())
+    for m, k, sign in ((1, 600, 1), (2, 0, -1)):
+        want = sign * torch.sign(w[:, k]) * math.inf  # 0 * inf: NaN
+        assert torch.equal(y[m].double().nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+    scratch = torch.empty(wq.wq_linear_logprobs_workspace_bytes(M, N), dtype=torch.uint8, device=dev())
+    lp, H, top, _ = wq.wq_linear_logprobs(x, pw, torch.zeros(M, dtype=torch.int32, device=dev()), 3, scratch,
+                                          ws=workspace(M, K, N, 8))
+    assert bool(lp[:3].isnan().all()) and bool(H[:3].isnan().all()) and bool(top[:3].isnan().all())
+    assert bool(lp[3:].isfinite().all()) and bool(H[3:].isfinite().all()) and bool(top[3:].isfinite().all())
+    assert wq.wq_device_error() == 0

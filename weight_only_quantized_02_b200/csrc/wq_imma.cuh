@@ -162,8 +162,12 @@ __device__ __forceinline__ void residual_add(unsigned long long *counter, int m,
 }
 
 // Bound on |y - y_exact| per unit of max|w| for token row m: units * 2^-24 * 2^-e_m.
+// A row that holds an infinity or a NaN (the largest finite bf16 has e = -106, they
+// -107) has digits that stand for nothing: no bound, every output recomputed.
 __device__ __forceinline__ double residual_bound(unsigned long long units, int e_m)
 {
+    if (e_m < -106)
+        return __longlong_as_double(0x7FF0000000000000ll);
     return (double)units * __longlong_as_double((long long)(1023 - 24 - e_m) << 52);
 }
 
@@ -216,7 +220,7 @@ __device__ __forceinline__ auto guard_tol(const Params &p)
 template <class Tol>
 __device__ __forceinline__ double row_bound(unsigned long long units, int e_m, const Tol &tol)
 {
-    return units <= tol.few && e_m < 127 ? 0.0 : residual_bound(units, e_m);
+    return units <= tol.few && e_m < 127 && e_m >= -106 ? 0.0 : residual_bound(units, e_m);
 }
 
 // Binary64 dot product of token row xm (bf16, K elements) with packed weight
