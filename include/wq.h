@@ -363,10 +363,12 @@ int wq_logprobs(const void *logits, int dtype, int M, int N, int64_t ld, const i
 
 /* wq_logprobs of the logits x . dequant(Wq)^T of a quantized vocabulary head,
  * which are formed in fp32 and never rounded to 16 bits or returned.  The integer
- * paths' logits are off by the larger of 2^-21 |logit| and max(4, K / 1024) 2^-21
- * max|x[m]| w at most (w as in wq_linear_epilogue), fp32 roundings aside; the logits
- * of a row with an element some 2^7 times the others' size are mostly formed again in
- * binary64, which takes longer.
+ * paths' logits are off by max(4, K / 1024) 2^-21 max|x[m]| w at most (w as in
+ * wq_linear_epilogue), fp32 roundings aside; where x held to 22 bits does not give
+ * that (a row with an element some 2^7 times the others' size, or with an infinity
+ * or a NaN), a second pass over the weight adds what is missing, which doubles the
+ * time, and they are off by 2^-21 |logit|.  (A workspace too small for it: those
+ * logits are formed one by one in binary64, and take many times as long.)
  *   scratch   device, at least wq_linear_logprobs_workspace_bytes(M, N) bytes,
  *             16-byte aligned, owned by the caller: the fp32 logits of up to
  *             512 tokens at a time, in turn

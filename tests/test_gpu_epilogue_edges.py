@@ -101,30 +101,108 @@ def outlier_case(bits, M, K, N, outlier, seed=0):
     return pw, w, x
 
 
-def rounded_sum(x):
-    """R: the row sums of what rounding to the integer kernels' units leaves over, in units."""
-    x = x.double()
-    unit = torch.exp2(torch.floor(torch.log2(x.abs().amax(1, keepdim=True))) - 21)
-    return (x / unit - torch.round(x / unit)).abs().sum(1)
+def unit_of(x):
+    """The integer kernels' unit of every row (include/wq.h), binary64 [M][1]."""
+    E = torch.floor(torch.log2(x.double().abs().amax(1, keepdim=True)))
+    return torch.exp2(-torch.clamp(21 - E, max=127))
 
 
-@pytest.mark.parametrize("bits,variant,M", [(8, 5, 1), (8, 5, 5), (8, 4, 16), (4, 5, 3), (4, 4, 9), (8, 4, 40)])
-def test_fp32_logits_of_outlier_rows(bits, variant, M):
-    """The head's logits are off by 2^-21 of their values at most in rows that the
-    fixed point form cannot hold, as sums in fp32 would be."""
-    K, N, k = 5120, 1040, 64
-    pw, w, x = outlier_case(bits, M, K, N, 2.0 ** 10)
-    assert float(rounded_sum(x).min()) > max(4, K // 1024)
+def needs_more(x):
+    """Rows that the integer kernels' form does not hold well enough as it is: R, what rounding
+    to their units leaves over, is above max(4, K / 1024), or the unit is held at 2^-127."""
+    q = x.double() / unit_of(x)
+    R = (q - torch.round(q)).abs().sum(1)
+    return (R > max(4, x.shape[1] // 1024)) | (unit_of(x)[:, 0] <= 2.0 ** -127)
+
+
+def group_sum_rounding(x, w, group=128):
+    """What INT4's fp32 sums over the groups may lose.  Every partial sum of a kernel is
+    within B = sum_i 256^i S_i units, S_i twice the largest prefix sum over the groups of
+    the i-th digits' products; it makes at most three roundings a group (two to
+    put the digits together, one to scale and add) and one for each of at most G
+    contributors, 2^-24 B each."""
+    M, K = x.shape
+    N, G = w.shape[0], K // group
+    X = torch.round(x.double() / unit_of(x))
+    B = torch.zeros((M, N), dtype=torch.float64, device=x.device)
+    for i in range(3):
+        d = torch.remainder(X + 128, 256) - 128
+        X = (X - d) / 256
+        t = torch.einsum("mgk,ngk->mng", d.view(M, G, group), w.view(N, G, group))
+        B += 256.0 ** i * 2 * t.cumsum(2).abs().amax(2)
+    return (4 * G + 8) * 2.0 ** -24 * B * unit_of(x)
+
+
+def check_fp32_logits(x, pw, w, bits, variant, ws_bytes=None):
+    """The logits that wq_linear_logprobs leaves in its scratch, against binary64:
+    2^-21 of their values (rows accepted whole: as many units of their largest as the
+    header allows), the rounding to fp32, and INT4's group sums."""
+    M, K = x.shape
+    N = w.shape[0]
     wq.wq_set_choice(M, K, N, bits, 128 if bits == 4 else 0, variant, 1)
     scratch = torch.empty(wq.wq_linear_logprobs_workspace_bytes(M, N), dtype=torch.uint8, device=dev())
-    wq.wq_linear_logprobs(x, pw, None, k, scratch, ws=workspace(M, K, N, 8))
+    ws = workspace(M, K, N, 8)
+    if ws_bytes is not None:
+        ws = ws[:ws_bytes]
+    t = torch.arange(M, dtype=torch.int32, device=dev())
     v = x.double() @ w.t()
-    logits = scratch.view(torch.float32).view(M, N).double()
-    # the rounding to fp32 is 2^-24 of the value; INT4's group sums are added in
-    # fp32 where the guard accepted them, which it does for none of these rows
-    tol = (2.0 ** -21 + 2.0 ** -23) * v.abs() + 2.0 ** -40
-    assert bool(((logits - v).abs() <= tol).all()), float(((logits - v).abs() / tol).max())
+    tol = (2.0 ** -21 + 2.0 ** -23) * v.abs() + 2.0 ** -149
+    # w's bound: 128 s where the codes reach 127 s, 8 s of 7.5 s at least
+    wmax = w.abs().amax(1) * 1.02 if bits == 8 else w.abs().max() * 1.1
+    tol = tol + (~needs_more(x)).double().unsqueeze(1) * max(4, K // 1024) * unit_of(x) * wmax
+    if bits == 4:
+        tol = tol + group_sum_rounding(x, w) * 1.01
+    first = None
+    for tokens, k in ((None, min(64, N)), (t, 0), (t, 3)):  # the flags' place differs
+        out = wq.wq_linear_logprobs(x, pw, tokens, k, scratch, ws=ws)
+        logits = scratch.view(torch.float32).view(M, N)
+        bad = ~((logits.double() - v).abs() <= tol)
+        assert not bad.any(), float(((logits.double() - v).abs() / tol).max())
+        first = logits.clone() if first is None else first
+        assert torch.equal(logits, first)
+        logp = torch.log_softmax(first.double(), 1)
+        if tokens is not None:
+            assert float((out[0].double() - logp.gather(1, t.long().unsqueeze(1)).squeeze(1)).abs().max()) <= 2.0 ** -16
+        assert float((out[1].double() + (logp.exp() * logp).sum(1)).abs().max()) <= 2.0 ** -17 * 12
+    assert int(ws[:262912].max()) == 0  # every counter back at zero
     assert wq.wq_device_error() == 0
+
+
+@pytest.mark.parametrize("bits,variant,M,K,outlier", [(8, 5, 1, 5120, 10), (8, 5, 5, 5120, 10), (8, 5, 5, 5120, 13),
+                                                      (8, 4, 16, 5120, 10), (8, 4, 40, 5120, 10), (8, 4, 64, 1056, 20),
+                                                      (4, 5, 3, 512, 11), (4, 5, 8, 512, 11), (4, 4, 9, 512, 11),
+                                                      (4, 4, 32, 512, 11), (4, 4, 1, 512, 14)])
+def test_fp32_logits_of_outlier_rows(bits, variant, M, K, outlier):
+    """The head's logits are off by 2^-21 of their values at most in rows that the
+    fixed point form cannot hold, in whichever kernel."""
+    pw, w, x = outlier_case(bits, M, K, 1040, 2.0 ** outlier)
+    if M > 2:
+        x[1, 5] = 1.0  # a row that is accepted whole, among the others
+    assert needs_more(x).tolist() == [m != 1 or M <= 2 for m in range(M)]
+    check_fp32_logits(x, pw, w, bits, variant)
+
+
+def test_fp32_logits_without_room_for_a_second_pass():
+    """A workspace that holds the integer GEMV's partial sums and no more: its
+    outputs are recomputed one by one."""
+    pw, w, x = outlier_case(8, 2, 512, 1040, 2.0 ** 12)
+    assert bool(needs_more(x).all())
+    check_fp32_logits(x, pw, w, 8, 5, 262912 + 448 * 8 * 2 * 16 * 8 * 4)
+
+
+def test_a_row_does_not_depend_on_the_others():
+    """A row's logits are the same bits beside rows that need the second pass."""
+    K, N, M = 1024, 1040, 9
+    pw, w, x = outlier_case(8, M, K, N, 2.0 ** 12)
+    x[::2, 5] = 0.5
+    wq.wq_set_choice(M, K, N, 8, 0, 4, 1)
+    scratch = torch.empty(wq.wq_linear_logprobs_workspace_bytes(M, N), dtype=torch.uint8, device=dev())
+    ws = workspace(M, K, N, 8)
+    wq.wq_linear_logprobs(x, pw, None, 1, scratch, ws=ws)
+    both = scratch.view(torch.float32).view(M, N).clone()
+    x[1::2, 5] = 0.5
+    wq.wq_linear_logprobs(x, pw, None, 1, scratch, ws=ws)
+    assert torch.equal(scratch.view(torch.float32).view(M, N)[::2], both[::2])
 
 
 @pytest.mark.parametrize("bits,variant,M", [(8, 5, 1), (8, 5, 5), (8, 4, 16), (4, 5, 3), (4, 4, 9)])
@@ -134,7 +212,7 @@ def test_multiplied_outputs_of_outlier_rows(bits, variant, M):
     the sum."""
     K, N = 5120, 2064
     pw, w, x = outlier_case(bits, M, K, N, 2.0 ** 10, 1)
-    assert float(rounded_sum(x).min()) > max(4, K // 1024)
+    assert bool(needs_more(x).all())
     mul = operands(M, K, N, torch.bfloat16, 1, False, True, False)[2] * 2.0 ** 12
     wq.wq_set_choice(M, K, N, bits, 128 if bits == 4 else 0, variant, 1)
     y = wq.wq_linear_epilogue(x, pw, mul=mul, ws=ws_for(M, K, N))
@@ -148,17 +226,10 @@ def test_multiplied_outputs_of_outlier_rows(bits, variant, M):
 @pytest.mark.parametrize("bits,variant,M", [(8, 5, 3), (8, 4, 16), (4, 5, 3), (4, 4, 9)])
 def test_fp32_logits_of_tiny_rows(bits, variant, M):
     """Rows around 2^-116, whose unit is held at 2^-127 (10 bits below the largest)."""
-    K, N, k = 512, 400, 20
+    K, N = 512, 400
     pw, w = make_weight(bits, 128 if bits == 4 else 0, K, N)
     x = (operands(M, K, N, torch.float32, 2, False, False, False)[0] * 2.0 ** -118).bfloat16()
-    wq.wq_set_choice(M, K, N, bits, 128 if bits == 4 else 0, variant, 1)
-    scratch = torch.empty(wq.wq_linear_logprobs_workspace_bytes(M, N), dtype=torch.uint8, device=dev())
-    wq.wq_linear_logprobs(x, pw, None, k, scratch, ws=workspace(M, K, N, 8))
-    v = x.double() @ w.t()
-    logits = scratch.view(torch.float32).view(M, N).double()
-    # as above; fp32's own roundings of values around 2^-120 are its subnormals' step, 2^-149
-    tol = (2.0 ** -21 + 2.0 ** -23) * v.abs() + 2.0 ** -149
-    assert bool(((logits - v).abs() <= tol).all()), float(((logits - v).abs() / tol).max())
+    check_fp32_logits(x, pw, w, bits, variant)
 
 
 # ---------------------------------------------------------------------------

@@ -284,16 +284,26 @@ int linear_chunk(const uint16_t *x, int M, int K, const void *Wq, const void *sc
         return WQ_ERR_VARIANT;
 
     LinearArgs a{x, M, K, N, Wq, scales, zeros, bits, bits == 8 ? 0 : lg, y, epi};
-    if (c.variant == WQ_VARIANT_GEMV_I8) {
-        if (!gi_ws_ok)
+    if (c.variant == WQ_VARIANT_GEMV_I8 || c.variant == WQ_VARIANT_I8MMA) {
+        const bool gemv = c.variant == WQ_VARIANT_GEMV_I8;
+        if (!(gemv ? gi_ws_ok : i8_ws_ok))
             return WQ_ERR_WORKSPACE;
-        return cuda_status(launch_gemv_i8(a, c.split, w, d.sm_count, stream));
-    }
-    if (c.variant == WQ_VARIANT_I8MMA) {
-        if (!i8_ws_ok)
-            return WQ_ERR_WORKSPACE;
-        return cuda_status(bits == 8 ? launch_gemm_i8(a, w, d.sm_count, stream)
-                                     : launch_gemm_i4(a, w, d.sm_count, stream));
+        // fp32 outputs: the integer tensor-core kernel is the second pass of both, where
+        // the workspace holds it (else the first recomputes output by output)
+        const bool flags = epi && epi->out_f32 && epi->rows, rest = flags && i8_ws_ok;
+        EpiArgs alone;
+        if (flags && !rest) {
+            alone = *epi;
+            alone.rows = nullptr;
+            a.epi = &alone;
+        }
+        const cudaError_t e = gemv        ? launch_gemv_i8(a, c.split, w, d.sm_count, stream)
+                              : bits == 8 ? launch_gemm_i8(a, w, d.sm_count, stream)
+                                          : launch_gemm_i4(a, w, d.sm_count, stream);
+        if (e != cudaSuccess || !rest)
+            return cuda_status(e);
+        return cuda_status(bits == 8 ? launch_gemm_i8_rest(a, w, d.sm_count, stream)
+                                     : launch_gemm_i4_rest(a, w, d.sm_count, stream));
     }
     if (c.variant == WQ_VARIANT_GEMV_RB)
         return cuda_status(launch_gemv(a, c.split, d.sm_count, stream));
@@ -384,6 +394,8 @@ EpiArgs epi_rows_from(const EpiArgs &e, int m0)
         r.mul += (long long)m0 * r.ld_mul;
     if (r.res)
         r.res += (long long)m0 * r.ld_res;
+    if (r.out_f32 && r.rows)
+        r.rows += m0 * r.rows_step;
     return r;
 }
 
@@ -861,6 +873,10 @@ int wq_linear_logprobs(const uint16_t *x, int M, int K, const void *Wq, const vo
     float *logits = static_cast<float *>(scratch);
     for (int m0 = 0; m0 < M; m0 += kHeadChunk) {
         const int mc = std::min(kHeadChunk, M - m0);
+        // flags of a second pass stand in an output of these rows until it is written
+        float *words = logprob ? logprob + m0 : entropy ? entropy + m0 : top_logprobs + (size_t)m0 * k;
+        e.rows = reinterpret_cast<int *>(words);
+        e.rows_step = logprob || entropy ? 1 : k;
         st = linear_impl(x + (size_t)m0 * K, mc, K, Wq, scales, zeros, group, N, reinterpret_cast<uint16_t *>(logits),
                          WQ_VARIANT_AUTO, 0, ws, ws_bytes_given, stream, &e);
         if (st != WQ_OK)

@@ -133,7 +133,8 @@ __device__ __forceinline__ float i4_epi_ops(const EpiArgs &e, int N, int n, int 
     return n < N ? epi_bias<true>(e, n) : 0.f;
 }
 
-template <int NR, bool EPI>
+// REST: the second pass of fp32 outputs (wq_imma.cuh).
+template <int NR, bool EPI, bool REST = false>
 // 14 warps: at most 4 per SM sub-partition, whose register file holds 16K
 // registers, so at most 128 per thread.
 __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p)
@@ -170,6 +171,12 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p
     const int KB = p.KB, M = p.M;
     const int u0 = sk_start(U, G, c), u1 = sk_start(U, G, c + 1);
     const int n = u1 - u0;
+
+    if constexpr (REST) {
+        pdl_wait(); // the flags and y are the preceding kernel's
+        if (!rest_any(p.epi, M, lane))
+            return; // the same in every warp of the grid
+    }
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SP; ++s) {
@@ -351,9 +358,12 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p
         pdl_wait(); // x, y and the workspace may come from / be in use by the preceding kernel
         const int et = threadIdx.x - 64; // 0..127
         const int quad = warp & 3;
-        imma_digit_phase<NR, true>(p.x, M, p.K, KB, c, G, et, p.xd, s_amax, s_e, p.grid, p.res);
+        imma_digit_phase<NR, true, REST>(p.x, M, p.K, KB, c, G, et, p.xd, s_amax, s_e, p.grid, p.res);
         const auto tol = guard_tol<EPI>(p);
-        ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb, tol) && ok;
+        if constexpr (REST)
+            ok = imma_rest_rows(M, G, et, p.grid, p.epi, s_e, s_rb) && ok;
+        else
+            ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb, tol, c) && ok;
         const double wmax = (double)__uint_as_float(__ldg(p.wmax));
 
         // ---------------- epilogue: one thread per output channel ----------------
@@ -411,11 +421,13 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p
                             bias = i4_epi_ops(p.epi, p.N, pnl * kPanelRows + row, M, ops);
 #pragma unroll
                         for (int m = 0; m < MM; ++m)
-                            if (m < M) // the same across the warp
+                            if (m < M && !(REST && s_rb[m] < 0.0)) // the same across the warp
                                 imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.K, KB, p.N,
                                                   pnl * kPanelRows + 32 * quad, m, (double)acc[m] * pow2_of(-s_e[m]),
                                                   wmax * s_rb[m], tol, lane, [&](int n, double y) {
-                                    if constexpr (EPI)
+                                    if constexpr (REST)
+                                        rest_store(p.y, p.N, m, n, y, s_rb[m]);
+                                    else if constexpr (EPI)
                                         epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[m]);
                                     else
                                         p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
@@ -458,11 +470,13 @@ __global__ void __maxnreg__(128) gemm_i4_kernel(const EpiParams<I4Params, EPI> p
                         bias = i4_epi_ops(p.epi, p.N, pnl * kPanelRows + row, M, ops);
 #pragma unroll
                     for (int m = 0; m < MM; ++m)
-                        if (m < M) // the same across the warp
+                        if (m < M && !(REST && s_rb[m] < 0.0)) // the same across the warp
                             imma_emit_rows<4>(p.x, p.wq, p.scales, p.zeros, p.K, KB, p.N,
                                               pnl * kPanelRows + 32 * quad, m, (double)tot[m] * pow2_of(-s_e[m]),
                                               wmax * s_rb[m], tol, lane, [&](int n, double y) {
-                                if constexpr (EPI)
+                                if constexpr (REST)
+                                    rest_store(p.y, p.N, m, n, y, s_rb[m]);
+                                else if constexpr (EPI)
                                     epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[m]);
                                 else
                                     p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
@@ -515,13 +529,13 @@ size_t ws_bytes_gemm_i4(int M, int K, int N)
     return ws_counter_bytes() + KB * NR * 128 + (size_t)kI8MaxCtas * 2 * (NR / 3) * 128 * sizeof(float);
 }
 
-template <int NR, bool EPI>
+template <int NR, bool EPI, bool REST = false>
 static cudaError_t launch_i4_e(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
 {
     constexpr size_t smem = i4_smem_bytes<NR>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
     {
-        const cudaError_t e = kernel_setup((const void *)gemm_i4_kernel<NR, EPI>, smem, 0, 0, nullptr);
+        const cudaError_t e = kernel_setup((const void *)gemm_i4_kernel<NR, EPI, REST>, smem, 0, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -558,7 +572,7 @@ static cudaError_t launch_i4_e(const LinearArgs &a, void *ws, int sm_count, cuda
     cfg.gridDim = dim3(G);
     cfg.blockDim = dim3(kI4Threads);
     cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelEx(&cfg, gemm_i4_kernel<NR, EPI>, p);
+    return cudaLaunchKernelEx(&cfg, gemm_i4_kernel<NR, EPI, REST>, p);
 }
 
 template <int NR>
@@ -574,6 +588,17 @@ cudaError_t launch_gemm_i4(const LinearArgs &a, void *ws, int sm_count, cudaStre
     case 32: return launch_i4_t<32>(a, ws, sm_count, st);
     case 48: return launch_i4_t<48>(a, ws, sm_count, st);
     case 96: return launch_i4_t<96>(a, ws, sm_count, st);
+    default: return cudaErrorInvalidValue; // M <= kI4MaxM
+    }
+}
+
+cudaError_t launch_gemm_i4_rest(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+{
+    switch (i8_digit_rows(a.M)) {
+    case 16: return launch_i4_e<16, true, true>(a, ws, sm_count, st);
+    case 32: return launch_i4_e<32, true, true>(a, ws, sm_count, st);
+    case 48: return launch_i4_e<48, true, true>(a, ws, sm_count, st);
+    case 96: return launch_i4_e<96, true, true>(a, ws, sm_count, st);
     default: return cudaErrorInvalidValue; // M <= kI4MaxM
     }
 }

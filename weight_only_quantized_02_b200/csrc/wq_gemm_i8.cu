@@ -113,7 +113,8 @@ __device__ __forceinline__ float i8_epi_ops(const EpiArgs &e, int N, int n, int 
     return n < N ? epi_bias<true>(e, n) : 0.f;
 }
 
-template <int NR, bool EPI>
+// REST: the second pass of fp32 outputs (wq_imma.cuh).
+template <int NR, bool EPI, bool REST = false>
 __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(const EpiParams<I8Params, EPI> p)
 {
     using C = I8Cfg<NR>;
@@ -140,6 +141,12 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
     const int KB = p.KB, M = p.M;
     const int u0 = sk_start(U, G, c), u1 = sk_start(U, G, c + 1);
     const int n = u1 - u0;
+
+    if constexpr (REST) {
+        pdl_wait(); // the flags and y are the preceding kernel's
+        if (!rest_any(p.epi, M, lane))
+            return; // the same in every warp of the grid
+    }
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -251,9 +258,12 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
         const int quad = warp & 3;
         const int K = p.K;
         // ---------------- activations: row maxima, then 1/G of the digit blocks ----------------
-        imma_digit_phase<NR>(p.x, M, K, KB, c, G, et, p.xd, s_amax, s_e, p.grid, p.res);
+        imma_digit_phase<NR, false, REST>(p.x, M, K, KB, c, G, et, p.xd, s_amax, s_e, p.grid, p.res);
         const auto tol = guard_tol<EPI>(p);
-        ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb, tol) && ok;
+        if constexpr (REST)
+            ok = imma_rest_rows(M, G, et, p.grid, p.epi, s_e, s_rb) && ok;
+        else
+            ok = imma_residual_bounds(M, G, et, p.grid, p.res, s_e, s_rb, tol, c) && ok;
         // ---------------- epilogue: one thread per output channel ----------------
         const int row = 32 * quad + lane;
         const uint32_t tq = (uint32_t)(32 * quad) << 16;
@@ -335,11 +345,13 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
 #pragma unroll
                     for (int t = 0; t < CG / 3; ++t) {
                         const int m = c0 / 3 + t; // the same across the warp
-                        if (m < M)
+                        if (m < M && !(REST && s_rb[m] < 0.0))
                             imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
                                               i8_value(v[3 * t], v[3 * t + 1], v[3 * t + 2], s_n * pow2_of(-s_e[m])),
                                               128.0 * s_n * s_rb[m], tol, lane, [&](int n, double y) {
-                                if constexpr (EPI)
+                                if constexpr (REST)
+                                    rest_store(p.y, p.N, m, n, y, s_rb[m]);
+                                else if constexpr (EPI)
                                     epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[t]);
                                 else
                                     p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
@@ -393,11 +405,13 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<NR>::kOcc) gemm_i8_kernel(co
 #pragma unroll
                 for (int t = 0; t < CG / 3; ++t) {
                     const int m = c0 / 3 + t; // the same across the warp
-                    if (m < M)
+                    if (m < M && !(REST && s_rb[m] < 0.0))
                         imma_emit_rows<8>(p.x, p.wq, p.scales, nullptr, K, KB, p.N, pnl * kPanelRows + 32 * quad, m,
                                           i8_value(tot[3 * t], tot[3 * t + 1], tot[3 * t + 2], s_n * pow2_of(-s_e[m])),
                                           128.0 * s_n * s_rb[m], tol, lane, [&](int n, double y) {
-                            if constexpr (EPI)
+                            if constexpr (REST)
+                                rest_store(p.y, p.N, m, n, y, s_rb[m]);
+                            else if constexpr (EPI)
                                 epi_store64<true>(p.epi, p.y, p.N, m, n, y, bias, ops[t]);
                             else
                                 p.y[(size_t)m * p.N + n] = __bfloat16_as_ushort(__double2bfloat16(y));
@@ -446,14 +460,14 @@ size_t ws_bytes_gemm_i8(int M, int K, int N)
     return ws_counter_bytes() + KB * NR * 128 + ctas * 2 * NR * 128 * sizeof(int32_t);
 }
 
-template <int NR, bool EPI>
+template <int NR, bool EPI, bool REST = false>
 static cudaError_t launch_i8_e(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
 {
     constexpr size_t smem = i8_smem_bytes<NR>();
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
     static_assert(I8Cfg<NR>::kOcc == 1 || 2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
     {
-        const cudaError_t e = kernel_setup((const void *)gemm_i8_kernel<NR, EPI>, smem, 0, 0, nullptr);
+        const cudaError_t e = kernel_setup((const void *)gemm_i8_kernel<NR, EPI, REST>, smem, 0, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -492,7 +506,7 @@ static cudaError_t launch_i8_e(const LinearArgs &a, void *ws, int sm_count, cuda
     cfg.gridDim = dim3(G);
     cfg.blockDim = dim3(kI8Threads);
     cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<NR, EPI>, p);
+    return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<NR, EPI, REST>, p);
 }
 
 template <int NR>
@@ -509,6 +523,17 @@ cudaError_t launch_gemm_i8(const LinearArgs &a, void *ws, int sm_count, cudaStre
     case 48: return launch_i8_t<48>(a, ws, sm_count, st);
     case 96: return launch_i8_t<96>(a, ws, sm_count, st);
     default: return launch_i8_t<192>(a, ws, sm_count, st);
+    }
+}
+
+cudaError_t launch_gemm_i8_rest(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st)
+{
+    switch (i8_digit_rows(a.M)) {
+    case 16: return launch_i8_e<16, true, true>(a, ws, sm_count, st);
+    case 32: return launch_i8_e<32, true, true>(a, ws, sm_count, st);
+    case 48: return launch_i8_e<48, true, true>(a, ws, sm_count, st);
+    case 96: return launch_i8_e<96, true, true>(a, ws, sm_count, st);
+    default: return launch_i8_e<192, true, true>(a, ws, sm_count, st);
     }
 }
 

@@ -636,6 +636,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_i8_kernel(const E
     pdl_launch_dependents();
     pdl_wait(); // x, y and the workspace may come from / be in use by the preceding kernel
     gi_digits<BITS, NR, WARPS * 32>(p, sd, s_dsum, s_amax, s_e, s_res);
+    if constexpr (EPI)
+        if (p.epi.out_f32 && p.epi.rows && c == 0 && (int)threadIdx.x < p.M)
+            guard_tol<true>(p).flag(threadIdx.x, s_res[threadIdx.x], s_e[threadIdx.x]);
 
     // ---------------- stream the warp's chunks ----------------
     int32_t acc_i[NT][4];

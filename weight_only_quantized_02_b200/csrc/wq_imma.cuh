@@ -178,6 +178,7 @@ __device__ __forceinline__ bool exact_enough(double y, double bound)
 
 // What the guard accepts of an output with value y and error bound `bound`.
 struct PlainTol {
+    static constexpr bool kEpi = false;
     static constexpr unsigned long long few = 0;
     __device__ __forceinline__ bool operator()(double y, double bound) const { return exact_enough(y, bound); }
 };
@@ -190,20 +191,40 @@ struct PlainTol {
 // the outputs near zero of every row would be recomputed.  few = max(4, K / 1024):
 // a row of K normally distributed values has R_m around K / 20000, and stays below it
 // with a largest element up to some 2^6 times the others' size.  (Not for rows
-// whose exponent is held at 127, where 2^-e is more than 2^-21 of the largest.)
+// whose exponent is held at 127, where 2^-e is more than 2^-21 of the largest, nor
+// for those with an infinity or a NaN.)
+//
+// fp32 outputs with a second pass to follow (EpiArgs::rows) are not recomputed one by
+// one: 2^-21 is too little for nearly every output of a row that is not accepted
+// whole (one token at the 5120 x 152064 head 1.4 ms in place of 0.13, 16 tokens 19 ms).
+// Such rows are flagged, and the pass adds what their rounding left over, exactly in
+// the same digits 22 bits further down.
 struct EpiTol {
+    static constexpr bool kEpi = true;
     double rel, least;
     unsigned long long few; // units of 2^-24
+    int *rows;              // flags of the second pass, NULL: none
+    long long rows_step;
     __device__ __forceinline__ EpiTol(const EpiArgs &e, int K)
     {
         const bool strict = e.out_f32 || e.mul;
         rel = e.out_f32 ? 1.0 / 2097152.0 : kExactTol;
         least = strict ? 0.0 : kExactTol;
         few = strict ? (unsigned long long)max(4, K >> 10) << 24 : 0ull;
+        rows = e.out_f32 ? e.rows : nullptr;
+        rows_step = e.rows_step;
     }
     __device__ __forceinline__ bool operator()(double y, double bound) const
     {
         return bound <= fmax(rel * fabs(y), least); // false for NaN: recomputed
+    }
+    __device__ __forceinline__ bool whole(unsigned long long units, int e_m) const
+    {
+        return units <= few && e_m < 127 && e_m >= -106;
+    }
+    __device__ __forceinline__ void flag(int m, unsigned long long units, int e_m) const
+    {
+        rows[m * rows_step] = !whole(units, e_m);
     }
 };
 
@@ -216,11 +237,14 @@ __device__ __forceinline__ auto guard_tol(const Params &p)
         return PlainTol();
 }
 
-// residual_bound, or 0 for a row that is accepted as it is.
+// residual_bound, or 0 for a row that is accepted whole or left to the second pass.
 template <class Tol>
 __device__ __forceinline__ double row_bound(unsigned long long units, int e_m, const Tol &tol)
 {
-    return units <= tol.few && e_m < 127 && e_m >= -106 ? 0.0 : residual_bound(units, e_m);
+    if constexpr (Tol::kEpi)
+        if (tol.rows || tol.whole(units, e_m))
+            return 0.0;
+    return residual_bound(units, e_m);
 }
 
 // Binary64 dot product of token row xm (bf16, K elements) with packed weight
@@ -398,7 +422,11 @@ __device__ __forceinline__ void imma_row_maxima(const uint16_t *__restrict__ x, 
 // tcgen05.st 16x256b from the packed INT4 tiles: in each 32-k step, byte
 // 8t + 4s + e holds k = 16s + 4t + e (the 4-byte words of the step's two
 // 16-k chunks interleaved).  An item is then a whole 32-k step.
-template <int NR, bool PAIRED = false>
+//
+// REST = true: the digits of what rounding to them leaves over, r = x 2^e - X
+// (|r| <= 1/2, of x's 8 significant bits at most, so exact as a bf16), in units of
+// 2^-22: round(r 2^22).  The residual sums are left alone.
+template <int NR, bool PAIRED = false, bool REST = false>
 __device__ __forceinline__ void imma_digit_phase(const uint16_t *__restrict__ x, int M, int K, int KB, int c, int G,
                                                  int et, uint8_t *xd, uint32_t *s_amax, int *s_e, uint32_t *grid,
                                                  unsigned long long *g_res)
@@ -455,10 +483,22 @@ __device__ __forceinline__ void imma_digit_phase(const uint16_t *__restrict__ x,
 #pragma unroll
             for (int h = 0; h < NV / 2; ++h) {
                 const uint4 &a = v[2 * h], &b = v[2 * h + 1];
-                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                float res = 0.f;
-                digit_planes(w, sc, pl[h], res);
-                units += residual_units(res);
+                uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                if constexpr (REST) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
+                        const float xl = fmaf(lo, sc, 12582912.0f) - 12582912.0f,
+                                    xh = fmaf(hi, sc, 12582912.0f) - 12582912.0f;
+                        w[i] = (__float_as_uint(fmaf(lo, sc, -xl)) >> 16) |
+                               (__float_as_uint(fmaf(hi, sc, -xh)) & 0xFFFF0000u);
+                    }
+                    digit_planes(w, 4194304.f, pl[h]); // 2^22
+                } else {
+                    float res = 0.f;
+                    digit_planes(w, sc, pl[h], res);
+                    units += residual_units(res);
+                }
             }
             if (units) // this CTA's share of the row's residual sum (exactness guard)
                 atomicAdd(&g_res[m], (unsigned long long)units);
@@ -492,11 +532,12 @@ __device__ __forceinline__ void imma_digit_phase(const uint16_t *__restrict__ x,
 
 // After the digit phase, by the same 128 threads: once every CTA has counted
 // itself on grid[0] (acquire, bounded), the residual bound of every token row
-// into s_rb (row_bound of the grid-wide sum).  False if the wait gave up.
+// into s_rb (row_bound of the grid-wide sum), and, by one CTA, the flags of a second
+// pass.  False if the wait gave up.
 template <class Tol>
 __device__ __forceinline__ bool imma_residual_bounds(int M, int G, int et, const uint32_t *grid,
                                                      const unsigned long long *g_res, const int *s_e, double *s_rb,
-                                                     const Tol &tol)
+                                                     const Tol &tol, int c)
 {
     bool ok = true;
     if (et < M) {
@@ -507,10 +548,58 @@ __device__ __forceinline__ bool imma_residual_bounds(int M, int G, int et, const
                 break;
             }
         }
-        s_rb[et] = ok ? row_bound(__ldcg(g_res + et), s_e[et], tol) : 0.0;
+        const unsigned long long units = __ldcg(g_res + et);
+        s_rb[et] = ok ? row_bound(units, s_e[et], tol) : 0.0;
+        if constexpr (Tol::kEpi)
+            if (tol.rows && c == 0)
+                tol.flag(et, units, s_e[et]);
     }
     named_barrier_sync(1, 128);
     return ok;
+}
+
+// ---- the second pass ----
+__device__ __forceinline__ bool rest_flag(const EpiArgs &e, int m)
+{
+    return __ldcg(e.rows + m * e.rows_step) != 0;
+}
+
+// Whether any row is flagged, by a whole warp.
+__device__ __forceinline__ bool rest_any(const EpiArgs &e, int M, int lane)
+{
+    bool any = false;
+    for (int m = lane; m < M; m += 32)
+        any = any || rest_flag(e, m);
+    return __any_sync(0xffffffffu, any) != 0;
+}
+
+// imma_residual_bounds of the second pass: s_rb is -1 for a row that is not flagged,
+// infinite for one that has no digits (every output recomputed), else 0; the exponents
+// become those of the digits.
+__device__ __forceinline__ bool imma_rest_rows(int M, int G, int et, const uint32_t *grid, const EpiArgs &e, int *s_e,
+                                               double *s_rb)
+{
+    bool ok = true;
+    if (et < M) {
+        const uint64_t t0 = globaltimer_ns();
+        while (ld_acquire_gpu(grid) < (uint32_t)G) {
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                ok = false;
+                break;
+            }
+        }
+        s_rb[et] = !ok || !rest_flag(e, et) ? -1.0 : s_e[et] < -106 ? residual_bound(0, s_e[et]) : 0.0;
+        s_e[et] += 22;
+    }
+    named_barrier_sync(1, 128);
+    return ok;
+}
+
+// Output (m, n) of the second pass: added, or in place of an output without digits.
+__device__ __forceinline__ void rest_store(uint16_t *y, int N, int m, int n, double v, double row)
+{
+    float *f = reinterpret_cast<float *>(y) + (size_t)m * N + n;
+    *f = (float)(row > 0.0 ? v : (double)__ldcg(f) + v);
 }
 
 } // namespace wq

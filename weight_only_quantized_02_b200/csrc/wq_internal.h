@@ -20,8 +20,18 @@ constexpr int kHeadChunk = 512; // tokens whose fp32 logits wq_linear_logprobs h
 // out_f32, the accumulated value itself as fp32 (y then points to floats).
 struct EpiArgs {
     const uint16_t *bias, *mul, *res;
-    long long ld_mul, ld_res; // row strides in elements
-    int act;                  // WQ_ACT_*
+    // Row strides in elements; with out_f32, which has no such operands, device words,
+    // rows_step apart, one a token row, where the integer kernels flag the rows
+    // that a second pass completes (NULL: no second pass).
+    union {
+        long long ld_mul;
+        long long rows_step;
+    };
+    union {
+        long long ld_res;
+        int *rows;
+    };
+    int act; // WQ_ACT_*
     int out_f32;
 };
 
@@ -121,6 +131,10 @@ cudaError_t read_gemm_w4_error(int *code, cudaStream_t st);
 
 // Integer tensor-core GEMM: ws >= ws_bytes_gemm_i8 / ws_bytes_gemm_i4 (always needed).
 cudaError_t launch_gemm_i8(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st);
+// Their second pass (a.epi->rows): adds to the fp32 outputs of the flagged rows what the
+// first, or the integer GEMV, rounded off their activations; nothing if there is none.
+cudaError_t launch_gemm_i8_rest(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st);
+cudaError_t launch_gemm_i4_rest(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st);
 cudaError_t read_gemm_i8_error(int *code, cudaStream_t st);
 size_t ws_bytes_gemm_i4(int M, int K, int N);
 cudaError_t launch_gemm_i4(const LinearArgs &a, void *ws, int sm_count, cudaStream_t st);
