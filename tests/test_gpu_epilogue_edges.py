@@ -265,3 +265,43 @@ def test_infinities_and_nan_in_a_row(bits, variant, split, M):
     assert bool(lp[:3].isnan().all()) and bool(H[:3].isnan().all()) and bool(top[:3].isnan().all())
     assert bool(lp[3:].isfinite().all()) and bool(H[3:].isfinite().all()) and bool(top[3:].isfinite().all())
     assert wq.wq_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# the activations' far tails
+# ---------------------------------------------------------------------------
+
+def activation64(v, act):
+    """The formulas in binary64, and the relative error of the kernels' evaluation: erf
+    GELU (2 + 1.4 a^2) 2^-22 at a = |v| / sqrt 2, whose own relative error of 0.36 2^-22
+    counts 2 a^2 = v^2 times, with two more products below (4 + 1.1 v^2) 2^-22; the
+    logistic forms' exponential (1 + 0.58 |u|) 2^-22, its sum, quotient and products,
+    and for tanh the five roundings of u, 1.25 2^-22 of |u|, below (4 + 2 |u|) 2^-22."""
+    if act == "gelu":
+        return 0.5 * v * torch.special.erfc(-v / math.sqrt(2)), (4 + 1.1 * v * v) * 2.0 ** -22
+    u = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    return v * torch.sigmoid(u), (4 + 2 * u.abs()) * 2.0 ** -22
+
+
+@pytest.mark.parametrize("act,far", [("gelu", 12.5), ("gelu_tanh", 8.5), ("silu", 92.0)])
+@pytest.mark.parametrize("bits,group,M,dtype", [(8, 0, 2, torch.bfloat16), (8, 0, 150, torch.bfloat16), (4, 128, 40, torch.bfloat16),
+                                                (4, 64, 3, torch.bfloat16), (8, 0, 9, torch.float16), (4, 32, 3, torch.float16)])
+def test_activations_keep_their_relative_accuracy(bits, group, M, dtype, act, far):
+    """Through zero and both tails, as long as the answer is a normal number of the
+    output's type: no error but the evaluation's, relative to the answer itself, and
+    its one rounding."""
+    K, N = 128, 4096
+    pw, _ = make_weight(bits, group, K, N)
+    x = torch.zeros((M, K), dtype=dtype, device=dev())
+    bias = torch.cat([torch.linspace(-far, far, N - 1024, device=dev()),
+                      torch.logspace(-3, math.log10(far), 1024, device=dev()) * -1]).to(dtype)
+    if dtype == torch.bfloat16:
+        y = wq.wq_linear_epilogue(x, pw, bias=bias, act=ACTS[act], ws=ws_for(M, K, N))
+    else:
+        y = wq.wq_linear_epilogue_f16(x, pw, bias=bias, act=ACTS[act])
+    ref, rel = activation64(bias.double(), act)
+    half = torch.finfo(dtype).eps / 2
+    normal = ref.abs() >= torch.finfo(dtype).smallest_normal * (1 + 2 * half)
+    tol = torch.where(normal, (rel + half * (1 + rel)) * ref.abs(), torch.finfo(dtype).smallest_normal * (1 + half))
+    assert bool((y.double() - ref <= tol).all()) and bool((ref - y.double() <= tol).all())
+    assert int(((bias < 0) & normal).sum()) > 900

@@ -102,9 +102,11 @@ __device__ __forceinline__ float epi_erfc(float a)
 
 // The activation of CNT values.  The erf form is written with erfc, which keeps
 // its relative accuracy where 1 + erf cancels; the tanh form is v * logistic(2 u),
-// which does not cancel either.  The logistic function uses the fast exponential
-// and division (a few 2^-22 of its value more per unit of |u|), against an output
-// of 8 or 11 significant bits.
+// which does not cancel either.  The logistic function is written with exp(-|u|), so
+// that the quotient's denominator stays between 1 and 2 (a fast division by exp(-u)
+// gives 0 from 2^126 on, where SiLU is still a normal number: -4e-37 at -88), and uses
+// the fast exponential and reciprocal (a few 2^-22 of its value, and one more per
+// unit of |u|), against an output of 8 or 11 significant bits.
 template <int CNT>
 __device__ __forceinline__ void epi_activations(float (&v)[CNT], int act)
 {
@@ -126,7 +128,10 @@ __device__ __forceinline__ void epi_activations(float (&v)[CNT], int act)
             float u = v[j]; // WQ_ACT_SILU: v * logistic(v)
             if (act == WQ_ACT_GELU_TANH)
                 u = 1.5957691f * fmaf(0.044715f * u, u * u, u); // 2 sqrt(2/pi) (v + 0.044715 v^3)
-            v[j] = __fdividef(v[j], 1.f + __expf(-u));
+            const float t = __expf(-fabsf(u));
+            float r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + t));
+            v[j] = (u < 0.f ? v[j] * t : v[j]) * r;
         }
     }
 }
