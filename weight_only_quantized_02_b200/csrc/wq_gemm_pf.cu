@@ -56,8 +56,8 @@
 // warps a scheduler; neither alone (a third of the retirement 320 us, no conversion
 // of the codes 327).
 //
-// Every wait is bounded (2 s); a timeout is recorded, every role winds down, and the
-// producers wait (as long at most) for their copies in flight before the CTAs leave.
+// Every wait is bounded (2 s); a timeout is recorded, every role winds down, and a
+// producer waits (as long at most) for its copies in flight before the CTAs leave.
 #include <atomic>
 #include <cstdint>
 
@@ -286,6 +286,17 @@ __device__ __forceinline__ int pf_owner(const PfParams &p, int G, int u)
             hi = mid - 1;
     }
     return lo;
+}
+
+// Waits (bounded) until the last of n copies into a ring of `stages` have landed: a
+// producer whose wait gave up does not leave them in flight behind its CTA.  (Of a
+// producer that came to its end the MMA issuer waits for every copy, or gives up
+// after longer than any takes.)
+__device__ __noinline__ void pf_landed(uint64_t *full, int stages, int n)
+{
+    for (int j = max(0, n - stages); j < n; ++j)
+        if (!mbar_wait(&full[j % stages], (j / stages) & 1))
+            return;
 }
 
 // What a retire warp needs to write a tile out.
@@ -605,11 +616,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
             const int half = p.n >> 1, tx = p.nsub * p.n * 128; // tx: both CTAs' bytes
             const uint32_t bar = pf_map(xfull, 0);
             int kb = kb0, tt = tile0 % p.TT;
-            int i = 0;
-            for (; i < 2 * nu; ++i) {
+            for (int i = 0; i < 2 * nu; ++i) {
                 const int xs = i % XS;
                 if (i >= XS && !mbar_wait(&done[xs], ((i / XS) - 1) & 1)) {
                     ok = false;
+                    if (rank == 0) // its barriers count both CTAs' bytes
+                        pf_landed(xfull, XS, i);
                     break;
                 }
                 if (rank == 0)
@@ -623,24 +635,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                         tt = 0;
                 }
             }
-            // Neither CTA leaves with a copy in flight, not after a wait that gave up
-            // either: the leader's barriers count both CTAs' bytes.
-            if (rank == 0)
-                for (int j = max(0, i - XS); j < i; ++j)
-                    if (!mbar_wait(&xfull[j % XS], (j / XS) & 1)) {
-                        ok = false;
-                        break;
-                    }
         } else if (warp == 1 && lane == 0) {
             // ---------------- weight producer ----------------
             const uint64_t pol = policy_evict_first();
             int kb = kb0, tt = tile0 % p.TT, pnl = 2 * (tile0 / p.TT) + (int)rank;
             int ws = 0;
             uint32_t wpar = 1; // the stage's last round; its first needs no wait
-            int i = 0;
-            for (; i < nu; ++i) {
+            for (int i = 0; i < nu; ++i) {
                 if (i >= WS && !mbar_wait(&wempty[ws], wpar)) {
                     ok = false;
+                    pf_landed(wfull, WS, i);
                     break;
                 }
                 const size_t blk = (size_t)pnl * KB + kb;
@@ -664,11 +668,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PfCfg<BITS>::kThread
                     }
                 }
             }
-            for (int j = max(0, i - WS); j < i; ++j) // as the x producer's
-                if (!mbar_wait(&wfull[j % WS], (j / WS) & 1)) {
-                    ok = false;
-                    break;
-                }
         } else if (warp == 2 && rank == 0) {
             // ---------------- MMA issuer ----------------
             // The whole warp walks the steps, so that addresses and descriptors
