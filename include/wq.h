@@ -261,10 +261,11 @@ typedef struct {
  *             the caller before its first use; calls that share one must not
  *             overlap), or NULL: the registered one
  * Up to 128 tokens the kernel is the dispatcher's, as in wq_linear, or the
- * prompt GEMM where a rule on the sizes finds it faster and wq_set_choice has not
- * named another; above 128 the prompt GEMM takes all tokens in one launch (INT4
- * groups stored as 128; other groups run 128 tokens at a time).  The prompt GEMM
- * uses as much of the workspace as it finds and needs none.
+ * prompt GEMM, or without a workspace the row-block GEMV, where a rule on the sizes
+ * finds it faster and wq_set_choice has not named another; above 128 the prompt
+ * GEMM takes all tokens in one launch (INT4 groups stored as 128; groups of 32 and
+ * 64 run 32 tokens at a time).  The prompt GEMM uses as much of the workspace as it
+ * finds and needs none.
  * WQ_ERR_EPILOGUE for an unknown act or a row stride below N. */
 int wq_linear_epilogue(const uint16_t *x, int M, int K, const void *Wq, const void *scales,
                        const void *zeros, int group, int N, const wq_epilogue *epilogue,

@@ -305,3 +305,37 @@ def test_activations_keep_their_relative_accuracy(bits, group, M, dtype, act, fa
     tol = torch.where(normal, (rel + half * (1 + rel)) * ref.abs(), torch.finfo(dtype).smallest_normal * (1 + half))
     assert bool((y.double() - ref <= tol).all()) and bool((ref - y.double() <= tol).all())
     assert int(((bias < 0) & normal).sum()) > 900
+
+
+# ---------------------------------------------------------------------------
+# calls without a workspace
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits,M,K,N", [(8, 9, 4096, 272), (8, 16, 8192, 144), (8, 32, 2048, 1040), (4, 9, 4096, 272),
+                                        (4, 32, 8192, 144), (8, 8, 4096, 272)])
+def test_long_k_and_few_channels_without_a_workspace(bits, M, K, N):
+    """Few tiles and nowhere to put partial sums: the row-block GEMV, which uses every SM, by
+    its bits (fp32 logits, so that another order of the sums would show); with a
+    workspace, and with a kernel chosen, the call is as before."""
+    group = 128 if bits == 4 else 0
+    pw, w = make_weight(bits, group, K, N)
+    x, bias, _, _ = operands(M, K, N, torch.bfloat16, 0, True, False, False)
+    scratch = torch.empty(wq.wq_linear_logprobs_workspace_bytes(M, N), dtype=torch.uint8, device=dev())
+
+    def logits(ws=None):
+        wq.wq_linear_logprobs(x, pw, None, 1, scratch, ws=ws)
+        return scratch.view(torch.float32).view(M, N).clone()
+
+    auto = logits()
+    by_split = []
+    for split in (1, 2, 4, 8):
+        wq.wq_set_choice(M, K, N, bits, group, wq.WQ_VARIANT_GEMV_RB, split)
+        by_split.append(torch.equal(auto, logits()))
+    assert any(by_split)
+    wq.wq_set_choice(M, K, N, bits, group, wq.WQ_VARIANT_GEMM, 1)
+    assert not torch.equal(auto, logits())
+    wq.wq_clear_tuning()
+    assert not torch.equal(auto, logits(workspace(M, K, N, 8)))
+    y = wq.wq_linear_epilogue(x, pw, bias=bias)
+    check(y, x, w, bias, "none", None, None, torch.bfloat16)
+    assert wq.wq_device_error() == 0

@@ -332,10 +332,11 @@ int linear_prompt(const uint16_t *x, int M, int K, const void *Wq, const void *s
                   const EpiArgs &epi);
 
 // Whether a call with an epilogue and at most 128 tokens goes to the prompt
-// GEMM, unless the caller chose a kernel for these sizes.  Measured on B200, us,
-// the layer's other kernels | the prompt GEMM:
+// GEMM, unless the caller chose a kernel for these sizes, where the workspace holds
+// what the layer's other kernels need.  Measured on B200, us, those | the prompt GEMM:
 //   INT8, 5120 x 17408: M = 9 28 | 31, 16 41 | 31, 64 92 | 32, 128 51 | 35;
-//   17408 x 5120: M = 9 43 | 40, 64 178 | 48; 1024 x 1024: M = 9 16 | 12, 64 62 | 13;
+//   17408 x 5120: M = 9 43 | 40 (goes with the row above: the border at 2^26 weights
+//   is its), 64 178 | 48; 1024 x 1024: M = 9 16 | 12, 64 62 | 13;
 //   a 5120 x 152064 head: M = 9 138 | 222, 32 180 | 227, 64 367 | 259 (the integer
 //   kernels stream a large weight faster, but take long to begin);
 //   INT4, 5120 x 17408: M = 64 37 | 41, 96 53 | 43, 128 53 | 43; 17408 x 5120:
@@ -352,25 +353,50 @@ bool prompt_faster(int bits, int M, int K, int N)
     return (M > 32 && codes <= (1LL << 23)) || (M > 64 && (N > 120 * kPanelRows || K <= 2048));
 }
 
+// Times of the two kernels that need no workspace, us, as measured on B200: a launch of
+// the row-block GEMV (32 tokens) 4 and 0.25 a million weights up to 8 tokens, 0.33 up to
+// 16, above that 0.5 (INT8) or 0.7 (INT4); the prompt GEMM on whole tiles 5 and 0.61 or
+// 0.8 for each 128 of K in each round of its tiles over the pairs of SMs.
+double row_block_us(int bits, int M, int K, int N)
+{
+    const double millions = (double)K * N * 1e-6, launch = 4 + millions * (bits == 8 ? 0.5 : 0.7);
+    const int rest = M % 32;
+    return M / 32 * launch + (rest > 16 ? launch : rest ? 4 + (rest > 8 ? 0.33 : 0.25) * millions : 0);
+}
+double whole_tiles_us(int bits, int M, int K, int N, int sm_count)
+{
+    const int pairs = std::max(1, std::min(sm_count / 2, kPfMaxPairs));
+    const int tok = bits == 8 ? 384 : 192;
+    const long long tiles = (long long)((N + 2 * kPanelRows - 1) / (2 * kPanelRows)) * ((M + tok - 1) / tok);
+    const double rounds = (double)((tiles + pairs - 1) / pairs), blocks = (double)((K + kBlockK - 1) / kBlockK);
+    return 5 + rounds * blocks * (bits == 8 ? 0.61 : 0.8);
+}
+
 // Whether an fp16 call with an epilogue goes to the prompt GEMM (whole tiles: that
-// entry has no workspace) or to the row-block GEMV's launches of 32 tokens, by the
-// times of both, us: a launch of the GEMV 4 and 0.25 a million weights up to 8 tokens,
-// 0.33 up to 16, above that 0.5 (INT8) or 0.7 (INT4); the prompt GEMM 5 and 0.61 or 0.8 for
-// each 128 of K in each round of its tiles over the pairs of SMs.  Measured on
+// entry has no workspace) or to the row-block GEMV's launches of 32 tokens.  Measured on
 // B200, GEMV | prompt GEMM: INT8 5120 x 17408 M = 4 26 | 29, 9 32 | 29, 64 101 | 32;
 // 17408 x 5120 M = 24 56 | 83, 64 120 | 83, 150 312 | 86; 4096 x 4096 M = 16 8 | 23;
 // 1024 x 1024 M = 300 50 | 10; INT4 5120 x 17408 M = 16 35 | 39, 32 70 | 39, 64
 // 138 | 40; 17408 x 5120 M = 32 74 | 109, 150 367 | 112; 4096 x 4096 M = 64 36 | 32.
 bool f16_prompt_faster(int bits, int M, int K, int N, int sm_count)
 {
-    const int pairs = std::max(1, std::min(sm_count / 2, kPfMaxPairs));
-    const int tok = bits == 8 ? 384 : 192;
-    const long long tiles = (long long)((N + 2 * kPanelRows - 1) / (2 * kPanelRows)) * ((M + tok - 1) / tok);
-    const double rounds = (double)((tiles + pairs - 1) / pairs), blocks = (double)((K + kBlockK - 1) / kBlockK);
-    const double millions = (double)K * N * 1e-6, launch = 4 + millions * (bits == 8 ? 0.5 : 0.7);
-    const int rest = M % 32;
-    const double gemv = M / 32 * launch + (rest > 16 ? launch : rest ? 4 + (rest > 8 ? 0.33 : 0.25) * millions : 0);
-    return 5 + rounds * blocks * (bits == 8 ? 0.61 : 0.8) < gemv;
+    return whole_tiles_us(bits, M, K, N, sm_count) < row_block_us(bits, M, K, N);
+}
+
+// Whether a call with an epilogue and 8 to 32 tokens that finds no room for the partial
+// sums of the layer's kernel goes to the row-block GEMV: its other choices, the prompt
+// GEMM on whole tiles and the GEMM unsplit, are bound by one tile's K (INT8 and INT4 alike
+// within a tenth of each other).  Measured on B200 without a workspace, row-block GEMV |
+// the better of them: INT8 17408 x 256 M = 16 25 | 84, 17408 x 1024 M = 32 31 | 85,
+// 4096 x 4096 M = 32 12 | 23, 5120 x 5120 M = 32 22 | 29, 17408 x 5120 M = 32 60 | 87,
+// 1024 x 1024 M = 9 3.4 | 8.5, 5120 x 17408 M = 9 32 | 34, 16 37 | 32, 32 45 | 33,
+// 5120 x 40960 M = 16 68 | 70, 32 107 | 74; INT4 17408 x 256 M = 16 17 | 111, 4096 x 4096 M = 32
+// 18 | 31, 17408 x 5120 M = 32 84 | 112, 2048 x 8192 M = 32 22 | 19, 5120 x 17408 M = 16 35 | 38,
+// 32 67 | 38.  The quarter more is for the rows in between, where its K slices cost more
+// than the model says.
+bool row_block_faster(int bits, int M, int K, int N, int sm_count)
+{
+    return M >= 8 && M <= 32 && 1.25 * row_block_us(bits, M, K, N) < whole_tiles_us(bits, M, K, N, sm_count);
 }
 
 // Whether the caller chose the kernel for these sizes (wq_set_choice).  An entry
@@ -413,9 +439,24 @@ int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *sca
     if (bits_of_group(group, &bits) != WQ_OK)
         return WQ_ERR_GROUP;
     const int chunk = chunk_tokens(bits, lgroup_of(bits, K, group));
-    if (epi && chunk == kChunkTokens && variant == WQ_VARIANT_AUTO &&
-        (M > kChunkTokens || (prompt_faster(bits, M, K, N) && !chosen(M, K, N, bits, group))))
-        return linear_prompt(x, M, K, Wq, scales, zeros, bits, group, N, y, ws, ws_bytes_given, stream, *epi);
+    if (epi && chunk == kChunkTokens && variant == WQ_VARIANT_AUTO) {
+        bool prompt = M > kChunkTokens;
+        if (!prompt && M >= 8 && K > 0 && N > 0 && !chosen(M, K, N, bits, group)) {
+            void *w = ws;
+            size_t have = ws_bytes_given;
+            if (!w)
+                registered_workspace(&w, &have);
+            // what the layer's default kernel of these sizes needs
+            const size_t need = bits == 8 && i8_fits(bits, M, K) ? ws_bytes_gemm_i8(M, K, N) : ws_bytes_gemm_sk(M, N);
+            DeviceInfo d;
+            if ((!w || have < need) && current_device_info(&d) == WQ_OK && row_block_faster(bits, M, K, N, d.sm_count))
+                variant = WQ_VARIANT_GEMV_RB;
+            else
+                prompt = prompt_faster(bits, M, K, N);
+        }
+        if (prompt)
+            return linear_prompt(x, M, K, Wq, scales, zeros, bits, group, N, y, ws, ws_bytes_given, stream, *epi);
+    }
     if (M <= chunk)
         return linear_chunk(x, M, K, Wq, scales, zeros, group, N, y, variant, split, ws, ws_bytes_given, stream, epi);
     if (M > kMaxTokens)
