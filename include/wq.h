@@ -356,8 +356,9 @@ size_t wq_topk_workspace_bytes(int M, int N, int k);
  * distribution: its log probabilities and entropy are NaN, its indices are
  * still those of the largest logits (a NaN above +inf).
  * 1 <= M <= 65536, 1 <= N <= 1048576.  Needs no workspace.  The
- * sums are taken in an order fixed by M, N, k and the device: equal calls give
- * equal bits.  WQ_ERR_NULL if nothing is asked for. */
+ * sums are taken in an order fixed by M, N, k, the type, the device and each
+ * row's address modulo 16 bytes: equal calls on the same buffers give equal bits.
+ * WQ_ERR_NULL if nothing is asked for. */
 int wq_logprobs(const void *logits, int dtype, int M, int N, int64_t ld, const int32_t *tokens,
                 int k, float *logprob, float *entropy, float *top_logprobs, int32_t *top_idx,
                 cudaStream_t stream);

@@ -390,10 +390,10 @@ bool f16_prompt_faster(int bits, int M, int K, int N, int sm_count)
 // the better of them: INT8 17408 x 256 M = 16 25 | 84, 17408 x 1024 M = 32 31 | 85,
 // 4096 x 4096 M = 32 12 | 23, 5120 x 5120 M = 32 22 | 29, 17408 x 5120 M = 32 60 | 87,
 // 1024 x 1024 M = 9 3.4 | 8.5, 5120 x 17408 M = 9 32 | 34, 16 37 | 32, 32 45 | 33,
-// 5120 x 40960 M = 16 68 | 70, 32 107 | 74; INT4 17408 x 256 M = 16 17 | 111, 4096 x 4096 M = 32
-// 18 | 31, 17408 x 5120 M = 32 84 | 112, 2048 x 8192 M = 32 22 | 19, 5120 x 17408 M = 16 35 | 38,
-// 32 67 | 38.  The quarter more is for the rows in between, where its K slices cost more
-// than the model says.
+// 5120 x 40960 M = 16 68 | 70, 32 107 | 74; INT4 17408 x 256 M = 16 17 | 111,
+// 4096 x 4096 M = 32 18 | 31, 17408 x 5120 M = 32 84 | 112, 2048 x 8192 M = 32 22 | 19,
+// 5120 x 17408 M = 16 35 | 38, 32 67 | 38.  The quarter more is for the sizes in
+// between, where its K slices cost more than the model says.
 bool row_block_faster(int bits, int M, int K, int N, int sm_count)
 {
     return M >= 8 && M <= 32 && 1.25 * row_block_us(bits, M, K, N) < whole_tiles_us(bits, M, K, N, sm_count);

@@ -112,7 +112,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity)
 
 // ---------------------------------------------------------------------------
 // Bulk (TMA engine) copies, global -> shared, completing on an mbarrier.
-// No multicast anywhere in this library.
+// No multicast copies anywhere in this library.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint64_t policy_evict_first()
 {

@@ -9,8 +9,8 @@
 //
 // Both terms of the entropy are positive (W <= 0, S >= 1), so it does not
 // cancel.  A thread keeps a running maximum with its S and W and rescales them
-// when the maximum grows, so every logit is read once and nothing is written
-// but the answers.
+// when the maximum grows, so the sums read every logit once (the alternatives read
+// a few again) and nothing is written but the answers.
 //
 // Bound: HBM, 2 or 4 bytes per logit.  At that rate an SM has to take 12
 // 16-bit logits a clock, three quarters of what its exponential unit can do
@@ -38,10 +38,11 @@
 // (Collecting during the loop, against a bound raised as it went, took 307 us
 // for 2048 rows of 152064 logits and k = 5.)
 //
-// Measured on B200: 2048 rows of 152064 bf16 logits 114 us without alternatives
-// (5.5 TB/s), 118 with 5 and 135 with 64 (168 with 5 where a mask leaves a few logits
-// a row); one such row with 20 alternatives 8.6; 77 rows of 50001 fp32 logits with 64
-// 15.5.
+// Measured on B200, back to back in a graph: 2048 rows of 152064 bf16 logits 114 us
+// without alternatives (5.5 TB/s), 118 with 5 and 135 with 64 (168 with 5 where a mask
+// leaves a few logits a row); one such row with 20 alternatives 8.6; 77 rows of 50001
+// fp32 logits with 64 15.5.  One call at a time from cold caches the 2048 rows take 133
+// with 5.
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     }
     if (lane == 0)
         sh.warp_sums[warp] = a;
-    __syncthreads(); // also: every candidate is in the list
+    __syncthreads(); // also: s_runs is written
     constexpr int W = THREADS / 32;
     Sums t = sh.warp_sums[lane & (W - 1)]; // every warp, the same sums in the same order
     t = butterfly(t, W);
