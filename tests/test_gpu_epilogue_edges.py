@@ -190,6 +190,57 @@ def test_fp32_logits_without_room_for_a_second_pass():
     check_fp32_logits(x, pw, w, 8, 5, 262912 + 448 * 8 * 2 * 16 * 8 * 4)
 
 
+@pytest.mark.parametrize("bits,variant,M,k", [(8, 5, 3, 3), (8, 4, 20, 64), (4, 4, 9, 7)])
+def test_second_pass_with_alternatives_alone(bits, variant, M, k):
+    """Neither tokens nor entropy asked for: the rows' flags stand among the alternatives."""
+    K, N = 512, 1040
+    pw, w, x = outlier_case(bits, M, K, N, 2.0 ** 12)
+    x[1, 5] = 1.0
+    wq.wq_set_choice(M, K, N, bits, pw.group, variant, 1)
+    nbytes = wq.wq_linear_logprobs_workspace_bytes(M, N)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev())
+    ws = workspace(M, K, N, 8)
+    want = wq.wq_linear_logprobs(x, pw, None, k, scratch, ws=ws)
+    logits = scratch.view(torch.float32).view(M, N).clone()
+    scratch.zero_()
+    top = torch.full((M + 1, k), 7.0, device=dev())
+    idx = torch.full((M + 1, k), 7, dtype=torch.int32, device=dev())
+    zeros = None if pw.zeros is None else pw.zeros.data_ptr()
+    rc = wq.lib.wq_linear_logprobs(x.data_ptr(), M, K, pw.wq.data_ptr(), pw.scales.data_ptr(), zeros, pw.group, N, None,
+                                   k, None, None, top.data_ptr(), idx.data_ptr(), scratch.data_ptr(), nbytes,
+                                   ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    assert torch.equal(scratch.view(torch.float32).view(M, N), logits)
+    assert torch.equal(top[:M], want[2]) and torch.equal(idx[:M], want[3])
+    assert bool((top[M] == 7).all()) and bool((idx[M] == 7).all())
+
+
+def test_second_pass_in_a_graph():
+    """Captured once, replayed with rows that need the second pass and rows that do not."""
+    K, N, M = 1024, 1040, 4
+    pw, w, x = outlier_case(8, M, K, N, 2.0 ** 12)
+    scratch = torch.empty(wq.wq_linear_logprobs_workspace_bytes(M, N), dtype=torch.uint8, device=dev())
+    ws = workspace(M, K, N, 8)
+    t = torch.arange(M, dtype=torch.int32, device=dev())
+    plain = x.clone()
+    plain[:, 5] = 0.5
+    want = [[o.clone() for o in wq.wq_linear_logprobs(v, pw, t, 5, scratch, ws=ws)] for v in (x, plain)]
+    held = x.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = wq.wq_linear_logprobs(held, pw, t, 5, scratch, ws=ws)
+    torch.cuda.synchronize()
+    for i in (1, 0, 0, 1, 0):
+        held.copy_((x, plain)[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+    assert int(ws[:262912].max()) == 0
+
+
 def test_a_row_does_not_depend_on_the_others():
     """A row's logits are the same bits beside rows that need the second pass."""
     K, N, M = 1024, 1040, 9

@@ -45,7 +45,7 @@
 // the products are done.
 //
 // Measured on B200 (layer with a residual or the other half of a gate, the weights
-// in L2): INT4 17408 x 5120, 2048 tokens 357 us (1020 TFLOP/s); 5120 x 17408, 364
+// in L2): INT4 17408 x 5120, 2048 tokens 360 us (1014 TFLOP/s); 5120 x 17408, 364
 // tokens 82; INT8 17408 x 5120, 2048 tokens 314 (1170 TFLOP/s); 5120 x 17408, 333
 // tokens 58.  In one launch of 2048 tokens the tensor pipe is busy in 70 % of the
 // cycles for INT8, at 1.57 GHz (back to back, the power limit holds the clock
