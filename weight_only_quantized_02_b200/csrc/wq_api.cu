@@ -440,8 +440,8 @@ int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *sca
         return WQ_ERR_GROUP;
     const int chunk = chunk_tokens(bits, lgroup_of(bits, K, group));
     if (epi && chunk == kChunkTokens && variant == WQ_VARIANT_AUTO) {
-        bool prompt = M > kChunkTokens;
-        if (!prompt && M >= 8 && K > 0 && N > 0 && !chosen(M, K, N, bits, group)) {
+        bool prompt = M > kChunkTokens, row_block = false;
+        if (!prompt && M >= 8 && K > 0 && N > 0) {
             void *w = ws;
             size_t have = ws_bytes_given;
             if (!w)
@@ -449,11 +449,14 @@ int linear_impl(const uint16_t *x, int M, int K, const void *Wq, const void *sca
             // what the layer's default kernel of these sizes needs
             const size_t need = bits == 8 && i8_fits(bits, M, K) ? ws_bytes_gemm_i8(M, K, N) : ws_bytes_gemm_sk(M, N);
             DeviceInfo d;
-            if ((!w || have < need) && current_device_info(&d) == WQ_OK && row_block_faster(bits, M, K, N, d.sm_count))
-                variant = WQ_VARIANT_GEMV_RB;
-            else
-                prompt = prompt_faster(bits, M, K, N);
+            row_block = (!w || have < need) && current_device_info(&d) == WQ_OK &&
+                        row_block_faster(bits, M, K, N, d.sm_count);
+            prompt = !row_block && prompt_faster(bits, M, K, N);
+            if ((row_block || prompt) && chosen(M, K, N, bits, group))
+                row_block = prompt = false;
         }
+        if (row_block && g_env_tuning == WQ_OK) // else the automatic choice reports it
+            variant = WQ_VARIANT_GEMV_RB;
         if (prompt)
             return linear_prompt(x, M, K, Wq, scales, zeros, bits, group, N, y, ws, ws_bytes_given, stream, *epi);
     }
